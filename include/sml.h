@@ -15,6 +15,13 @@
  *                          the producers just before the step: FP8
  *                          quantisation of new tokens into the two caches,
  *                          and of the indexer queries
+ *   sml_paged_mla_decode   absorbed-query MLA over every cached token, or the
+ *                          last W of them (a sliding-window layer)
+ *   sml_block_keys_write, sml_block_scores, sml_block_topk,
+ *   sml_block_mla_decode   selection by whole pages: one key per page, its
+ *                          score per query, the best pages, and MLA over them
+ *   sml_latent_cache_read, sml_indexer_k_cache_read
+ *                          cached rows back as bf16
  *   sml_dcp_pack_candidates, sml_dcp_merge_candidates,
  *   sml_dcp_split_selection, sml_lse_combine
  *                          decode context parallelism: the steps between the
@@ -101,6 +108,7 @@ extern "C" {
 #define SML_STAGE_TOPK 2
 #define SML_STAGE_MLA 3
 #define SML_STAGE_LAYER 4
+#define SML_STAGE_PAGED 5   /* sml_paged_mla_decode and sml_block_mla_decode */
 
 /* One batch of query tokens.  Host struct; the pointers in it are device
  * pointers.  Every entry point validates it. */
@@ -278,6 +286,79 @@ int sml_sparse_mla_decode_noalloc(const sml_problem* p, const void* q, sml_cache
  * Allocates nothing.  (The pages have no counterpart.) */
 int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
 
+/* ---- attention over the whole cache, or over selected pages ----------------
+ *
+ * vLLM blog "vLLM 首日支持 Mistral Large 4", section on DSpark: the draft layers
+ * are sliding-window (2,048-token) MLA layers over a bf16 cache; highlights
+ * list: MLA with KV LoRA rank 512 and RoPE dim 64.  Layers without an indexer
+ * attend to every cached token.  Choosing whole 64-token pages instead of
+ * single tokens scores one key per page: 1/64 of the indexer's scan, and the
+ * attention reads contiguous pages.  (The pages print no block selection; it
+ * is this library's own form of the DSA indexer.) */
+
+/* MLA over the paged cache.  For token t, head h and positions
+ * i in [max(0, n_t - window), n_t) (window = 0: every i in [0, n_t)):
+ *   z_i = sm_scale * c_t * (q[t,h,0:512] . c_hat_i + q[t,h,512:576] . k_pe_i)
+ *   out[t,h,:] = sum_i softmax(z)_i * c_hat_i,  lse[t,h] = ln sum_i exp(z_i)
+ * with c_hat_i and c_t as in sml_sparse_mla_decode (c_t's n is n_t, or
+ * ssmax_len, whatever the window).  p->topk is checked but not used.
+ *   q    [T, H, 512 + rope_dim] bf16 (16-B aligned)
+ *   out  [T, H, 512] bf16 (16-B aligned; the operand of the value projection)
+ *   lse  [T, H] fp32 (natural log)
+ * A token that sees nothing (n_t = 0, or its request's lengths are bad) gets
+ * out = 0 and lse = -inf.  What cached rows hold at or past n_t, or before the
+ * window, never matters, NaN included.  The products, the row sums and the
+ * accumulated outputs are fp32; each softmax weight enters its product with at
+ * least 8 significant bits, as a bf16 has.  Positions in a page outside the
+ * pool are masked (SML_FAULT_PAGE).
+ * Workspace: SML_STAGE_PAGED.  Nothing in it has to survive between calls. */
+int sml_paged_mla_decode(const sml_problem* p, const void* q, sml_cache latent, int32_t window, void* out,
+                         float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* The same over the listed blocks of each token: block j is positions
+ * [64 j, min(64 j + 64, n_t)) of its request (one page).
+ *   blocks      [T, max_blocks] int32, 1 <= max_blocks <= 2^24: logical page
+ *               numbers in any order; the first blocks_len[t] of a row are read
+ *   blocks_len  [T] int32, in [0, max_blocks] (outside: clamped, SML_FAULT_TOPK_LEN)
+ * A block outside [0, ceil(n_t / 64)) is masked (SML_FAULT_INDEX); one listed
+ * twice counts twice.  No listed block: out = 0, lse = -inf. */
+int sml_block_mla_decode(const sml_problem* p, const void* q, sml_cache latent, const int32_t* blocks,
+                         const int32_t* blocks_len, int32_t max_blocks, void* out, float* lse, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* Block keys: for every listed physical page of the indexer cache, the mean of
+ * its 64 dequantised keys (summed in 64 bits, rounded to fp32), stored as the
+ * producers below store a key: s = amax / 448 (1 when amax = 0) and the E4M3
+ * codes of mean / s.  block_cache is a pool in the indexer layout whose row p
+ * (page p / 64, row p % 64) is the block key of page p of index_cache; it needs
+ * index_cache.num_pages rows.  A page is listed once all its 64 rows are
+ * written.  pages[i] = -1 skips; a page outside [0, index_cache.num_pages) is
+ * skipped and sets SML_FAULT_PAGE (workspace NULL or >= 256 B).  A page listed
+ * twice is written twice with the same bytes.  n = 0 is a no-op. */
+int sml_block_keys_write(sml_cache index_cache, const int32_t* pages, int32_t n, sml_cache block_cache,
+                         void* workspace, void* stream);
+
+/* Block scores: the indexer's formula with block keys,
+ *   S[t, j] = c_t * sq_t * sb_j * sum_h w[t, h] * ReLU(sum_d e4m3(q8[t,h,d]) * e4m3(kb8_j[d]))
+ * for the blocks j < (n_t - 1) / 64 (integer division) that lie wholly before
+ * the block of the token's newest position; kb8_j, sb_j: row
+ * block_table[r, j] of block_cache.  iq8, iq_scale, iw as in
+ * sml_indexer_scores.  scores [T, max_pages] fp32; other entries are not
+ * written.  A page outside block_cache scores NaN (which ranks last) and sets
+ * SML_FAULT_PAGE (workspace NULL or >= 256 B).  FP8 products are exact; sums
+ * accumulate in fp32. */
+int sml_block_scores(const sml_problem* p, const void* iq8, const float* iq_scale, const float* iw,
+                     sml_cache block_cache, float* scores, void* workspace, void* stream);
+
+/* Block selection: for every token the num_blocks - 1 best of the blocks
+ * j < (n_t - 1) / 64 by scores [T, max_pages] (the order of sml_topk: larger
+ * first, -0.0 == +0.0, NaN last, equal scores to the lower block), ascending,
+ * then the block of its newest position, (n_t - 1) / 64.
+ *   blocks      [T, num_blocks] int32 out, 1 <= num_blocks <= 2048, -1 padding
+ *   blocks_len  [T] int32 out (0 when the token sees nothing) */
+int sml_block_topk(const sml_problem* p, const float* scores, int32_t num_blocks, int32_t* blocks,
+                   int32_t* blocks_len, void* workspace, void* stream);
+
 /* ---- producers: quantise new tokens and write the caches the step reads ----
  *
  * vLLM blog "vLLM 首日支持 Mistral Large 4", paragraph "可断开的 CUDA 图和融合":
@@ -311,6 +392,19 @@ int sml_indexer_k_cache_write(const void* k, const int32_t* slot, int32_t n, sml
  * given (c, then k_pe). */
 int sml_latent_cache_write(const void* c, const void* k_pe, const int32_t* slot, int32_t n,
                            sml_cache latent, void* workspace, void* stream);
+
+/* Reading cached rows back, the writers' counterparts: row i of the output is
+ * the cached row slot[i] = physical page * 64 + row, dequantised in fp32 and
+ * rounded to bf16 once (a bf16 pool's values as they are).  slot[i] = -1 leaves
+ * row i as it was; a slot outside [-1, num_pages * 64) does too and sets
+ * SML_FAULT_PAGE (workspace NULL or >= 256 B).  A slot may be named more than
+ * once.  n = 0 is a no-op.
+ *   c [n, 512] bf16, k_pe [n, 64] bf16 (NULL: not read), k [n, 128] bf16, all
+ *   16-B aligned */
+int sml_latent_cache_read(const int32_t* slot, int32_t n, sml_cache latent, void* c, void* k_pe, void* workspace,
+                          void* stream);
+int sml_indexer_k_cache_read(const int32_t* slot, int32_t n, sml_cache index_cache, void* k, void* workspace,
+                             void* stream);
 
 /* Indexer Q path: iq [T, 64, 128] bf16 (16-B aligned) -> iq8 [T, 64, 128]
  * e4m3 codes (16-B aligned) and iq_scale [T] fp32, one block per token: the

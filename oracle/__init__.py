@@ -13,6 +13,7 @@ Modules:
   dsa     -- indexer scores, visible lengths, exact top-k
   mla     -- absorbed-query attention, sparse and dense MLA, LSE merge, one layer
   producers -- FP8 quantisation and the cache writes just before the step
+  blocks  -- block keys, block scores, block selection, reading cached rows back
   dcp     -- the step with the cache sharded by token over ranks (decode
              context parallelism): candidates, stable merge, LSE combine
 
@@ -20,4 +21,4 @@ Every function is pinned by tests under ``tests/`` (``-m "not gpu"``) to
 values the pages print, closed forms, invariants, library routines and brute
 force on tiny inputs; none is "parity unpinned".
 """
-from . import dcp, dsa, formats, mla, producers  # noqa: F401
+from . import blocks, dcp, dsa, formats, mla, producers  # noqa: F401

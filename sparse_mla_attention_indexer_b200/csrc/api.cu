@@ -94,6 +94,25 @@ struct Layout {
          scores = 0, total = 0;
 };
 
+// The paged-MLA workspace: [header][top-k counters, untouched][joins][partials].
+// It keeps the counters' place, so a workspace that serves both forms of
+// attention keeps them zero; its size depends on the heads and the device, not
+// on the batch or the context.
+struct PagedLayout {
+  size_t join, part_out, part_lse, total;
+};
+
+PagedLayout paged_layout(const sml_problem& p) {
+  PagedLayout L;
+  const PagedWs w = paged_plan(p);
+  const size_t rows = (size_t)w.hg * w.cpg * 2 * paged_heads(p);
+  L.join = align_up(sizeof(WsHeader)) + align_up((size_t)65536 * sizeof(int32_t));
+  L.part_out = L.join + align_up((size_t)w.hg * w.cpg * sizeof(int4));
+  L.part_lse = L.part_out + align_up(rows * SML_LATENT_DIM * sizeof(float));
+  L.total = L.part_lse + align_up(rows * sizeof(float));
+  return L;
+}
+
 int topk_chunks(const sml_problem& p) { return (p.max_ctx + kTopkChunk - 1) / kTopkChunk; }
 
 // One fixed layout for every stage: [header][top-k counters][top-k candidates]
@@ -141,7 +160,7 @@ void check_workspace(Checker& c, const sml_problem* p, int stage, void* ws, size
   }
   if (!aligned(ws, 256)) c.fail(SML_ERR_WORKSPACE, "workspace not 256-B aligned");
   if (p && c.code == SML_OK) {
-    const size_t need = layout(*p, stage).total;
+    const size_t need = stage == SML_STAGE_PAGED ? paged_layout(*p).total : layout(*p, stage).total;
     if (bytes < need) {
       char buf[128];
       snprintf(buf, sizeof buf, "workspace has %zu bytes, needs %zu", bytes, need);
@@ -219,9 +238,10 @@ extern "C" {
 size_t sml_workspace_size(const sml_problem* p, int stage) {
   Checker c;
   check_problem(c, p);
-  c.check(stage >= SML_STAGE_INDEXER && stage <= SML_STAGE_LAYER, SML_ERR_INVALID_ARG,
+  c.check(stage >= SML_STAGE_INDEXER && stage <= SML_STAGE_PAGED, SML_ERR_INVALID_ARG,
           "stage not one of SML_STAGE_*");
   if (c.done("sml_workspace_size") != SML_OK) return 0;
+  if (stage == SML_STAGE_PAGED) return paged_layout(*p).total;
   return layout(*p, stage).total;
 }
 
@@ -390,6 +410,125 @@ int sml_indexer_q_quant(const void* iq, int32_t num_tokens, void* iq8, float* iq
   if (c.done("sml_indexer_q_quant") != SML_OK) return c.code;
   cudaError_t e = launch_indexer_q_quant(iq, num_tokens, iq8, iq_scale, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SML_OK : cuda_fail(e, "sml_indexer_q_quant");
+}
+
+int sml_latent_cache_read(const int32_t* slot, int32_t n, sml_cache latent, void* cl, void* k_pe, void* workspace,
+                          void* stream) {
+  Checker c;
+  check_producer(c, n, slot, latent, "latent", kMaxSlotPages, workspace, true);
+  c.check(n == 0 || (cl != nullptr && aligned(cl, 16)), SML_ERR_INVALID_ARG, "c NULL or not 16-B aligned");
+  c.check(aligned(k_pe, 16), SML_ERR_INVALID_ARG, "k_pe not 16-B aligned");
+  if (c.done("sml_latent_cache_read") != SML_OK) return c.code;
+  cudaError_t e = launch_latent_read(slot, n, latent, cl, k_pe, workspace ? status_of(workspace) : nullptr,
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SML_OK : cuda_fail(e, "sml_latent_cache_read");
+}
+
+int sml_indexer_k_cache_read(const int32_t* slot, int32_t n, sml_cache index_cache, void* k, void* workspace,
+                             void* stream) {
+  Checker c;
+  check_producer(c, n, slot, index_cache, "index_cache", kMaxSlotPages, workspace, false);
+  c.check(n == 0 || (k != nullptr && aligned(k, 16)), SML_ERR_INVALID_ARG, "k NULL or not 16-B aligned");
+  if (c.done("sml_indexer_k_cache_read") != SML_OK) return c.code;
+  cudaError_t e = launch_indexer_k_read(slot, n, index_cache, k, workspace ? status_of(workspace) : nullptr,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SML_OK : cuda_fail(e, "sml_indexer_k_cache_read");
+}
+
+// ---- attention over the whole cache, or over selected pages ----------------------------
+
+namespace {
+
+int paged_mla(const char* fn, Checker& c, const sml_problem* p, const void* q, sml_cache latent, const PagedSel& sel,
+              void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  c.check(q != nullptr && aligned(q, 16), SML_ERR_INVALID_ARG, "q NULL or not 16-B aligned");
+  c.check(out != nullptr && aligned(out, 16), SML_ERR_INVALID_ARG, "out NULL or not 16-B aligned");
+  c.check(lse != nullptr, SML_ERR_INVALID_ARG, "lse is NULL");
+  check_cache(c, latent, "latent", true);
+  c.check(latent.num_pages <= kMaxSlotPages, SML_ERR_UNSUPPORTED, "latent.num_pages * 64 rows exceed int32");
+  check_workspace(c, p, SML_STAGE_PAGED, workspace, ws_bytes);
+  if (c.done(fn) != SML_OK) return c.code;
+  const PagedLayout L = paged_layout(*p);
+  char* b = static_cast<char*>(workspace);
+  PagedWs w = paged_plan(*p);
+  w.join = reinterpret_cast<int4*>(b + L.join);
+  w.part_out = reinterpret_cast<float*>(b + L.part_out);
+  w.part_lse = reinterpret_cast<float*>(b + L.part_lse);
+  cudaError_t e = launch_paged_mla(*p, static_cast<const uint16_t*>(q), latent, sel, static_cast<uint16_t*>(out), lse,
+                                   w, status_of(workspace), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SML_OK : cuda_fail(e, fn);
+}
+
+}  // namespace
+
+int sml_paged_mla_decode(const sml_problem* p, const void* q, sml_cache latent, int32_t window, void* out,
+                         float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  Checker c;
+  check_problem(c, p);
+  c.check(window >= 0, SML_ERR_INVALID_ARG, "window < 0");
+  return paged_mla("sml_paged_mla_decode", c, p, q, latent, PagedSel{window, nullptr, nullptr, 0}, out, lse, workspace,
+                   ws_bytes, stream);
+}
+
+int sml_block_mla_decode(const sml_problem* p, const void* q, sml_cache latent, const int32_t* blocks,
+                         const int32_t* blocks_len, int32_t max_blocks, void* out, float* lse, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  Checker c;
+  check_problem(c, p);
+  c.check(blocks != nullptr, SML_ERR_INVALID_ARG, "blocks is NULL");
+  c.check(blocks_len != nullptr, SML_ERR_INVALID_ARG, "blocks_len is NULL");
+  c.check(max_blocks >= 1, SML_ERR_INVALID_ARG, "max_blocks < 1");
+  c.check(max_blocks <= (1 << 24), SML_ERR_UNSUPPORTED, "max_blocks > 2^24");
+  return paged_mla("sml_block_mla_decode", c, p, q, latent, PagedSel{0, blocks, blocks_len, max_blocks}, out, lse,
+                   workspace, ws_bytes, stream);
+}
+
+int sml_block_keys_write(sml_cache index_cache, const int32_t* pages, int32_t n, sml_cache block_cache,
+                         void* workspace, void* stream) {
+  Checker c;
+  c.check(n >= 0, SML_ERR_INVALID_ARG, "n < 0");
+  c.check(n == 0 || (pages != nullptr && aligned(pages, 4)), SML_ERR_INVALID_ARG, "pages NULL or not 4-B aligned");
+  check_cache(c, index_cache, "index_cache", false);
+  check_cache(c, block_cache, "block_cache", false);
+  c.check(index_cache.num_pages <= INT32_MAX, SML_ERR_UNSUPPORTED, "index_cache.num_pages exceeds int32");
+  c.check((index_cache.num_pages + SML_PAGE_TOKENS - 1) / SML_PAGE_TOKENS <= block_cache.num_pages,
+          SML_ERR_INVALID_ARG, "block_cache has fewer rows than index_cache has pages");
+  c.check(workspace == nullptr || aligned(workspace, 256), SML_ERR_WORKSPACE, "workspace not 256-B aligned");
+  if (c.done("sml_block_keys_write") != SML_OK) return c.code;
+  cudaError_t e = launch_block_keys(index_cache, pages, n, block_cache, workspace ? status_of(workspace) : nullptr,
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SML_OK : cuda_fail(e, "sml_block_keys_write");
+}
+
+int sml_block_scores(const sml_problem* p, const void* iq8, const float* iq_scale, const float* iw,
+                     sml_cache block_cache, float* scores, void* workspace, void* stream) {
+  Checker c;
+  check_problem(c, p);
+  c.check(iq8 != nullptr && aligned(iq8, 16), SML_ERR_INVALID_ARG, "iq8 NULL or not 16-B aligned");
+  c.check(iq_scale != nullptr, SML_ERR_INVALID_ARG, "iq_scale is NULL");
+  c.check(iw != nullptr && aligned(iw, 16), SML_ERR_INVALID_ARG, "iw NULL or not 16-B aligned");
+  c.check(scores != nullptr, SML_ERR_INVALID_ARG, "scores is NULL");
+  check_cache(c, block_cache, "block_cache", false);
+  c.check(workspace == nullptr || aligned(workspace, 256), SML_ERR_WORKSPACE, "workspace not 256-B aligned");
+  if (c.done("sml_block_scores") != SML_OK) return c.code;
+  cudaError_t e = launch_block_scores(*p, static_cast<const uint8_t*>(iq8), iq_scale, iw, block_cache, scores,
+                                      workspace ? status_of(workspace) : nullptr, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SML_OK : cuda_fail(e, "sml_block_scores");
+}
+
+int sml_block_topk(const sml_problem* p, const float* scores, int32_t num_blocks, int32_t* blocks,
+                   int32_t* blocks_len, void* workspace, void* stream) {
+  Checker c;
+  check_problem(c, p);
+  c.check(scores != nullptr, SML_ERR_INVALID_ARG, "scores is NULL");
+  c.check(num_blocks >= 1 && num_blocks <= SML_MAX_TOPK, SML_ERR_UNSUPPORTED, "num_blocks not in [1, 2048]");
+  c.check(blocks != nullptr, SML_ERR_INVALID_ARG, "blocks is NULL");
+  c.check(blocks_len != nullptr, SML_ERR_INVALID_ARG, "blocks_len is NULL");
+  c.check(workspace == nullptr || aligned(workspace, 256), SML_ERR_WORKSPACE, "workspace not 256-B aligned");
+  if (c.done("sml_block_topk") != SML_OK) return c.code;
+  cudaError_t e = launch_block_topk(*p, scores, num_blocks, blocks, blocks_len,
+                                    workspace ? status_of(workspace) : nullptr, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SML_OK : cuda_fail(e, "sml_block_topk");
 }
 
 // ---- decode context parallelism -------------------------------------------------------

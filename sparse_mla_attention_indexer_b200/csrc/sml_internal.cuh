@@ -63,6 +63,34 @@ struct MlaWs {
   MlaPlan plan;
 };
 
+// Paged MLA work split.  A unit is (query token, group of kPagedHeads heads,
+// tile of two pages); a token has at least one tile, so that a token with
+// nothing to attend to still has a CTA that writes its empty result.  The tile
+// counts follow from device data, so every CTA works out its range itself:
+// head group g is served by the CTAs with blockIdx.x % hg == g, and those share
+// the group's tiles (token-major) in equal contiguous ranges.  A CTA writes a
+// token that lies wholly in its range straight to the output; of the others it
+// holds at most two pieces, one at each end of its range, which go to its two
+// partial slots and are joined by the merge: slot 0 for a piece that does not
+// begin its token, slot 1 for one that does.
+struct PagedWs {
+  int4* join;          // [ctas] {token, first CTA, last CTA} of the token to join at this CTA, token -1: none
+  float* part_out;     // [ctas * 2 * heads per unit, 512]
+  float* part_lse;     // [ctas * 2 * heads per unit]
+  int hg;              // head groups
+  int cpg;             // CTAs per head group
+};
+PagedWs paged_plan(const sml_problem& p);          // hg and cpg of a problem on the current device
+int paged_heads(const sml_problem& p);             // heads per unit
+// The attention's inputs besides the problem: blocks == nullptr reads the
+// whole visible context (window > 0: its end), else the listed blocks.
+struct PagedSel {
+  int window;
+  const int32_t* blocks;
+  const int32_t* blocks_len;
+  int max_blocks;
+};
+
 // Message returned by sml_last_error() on this host thread.
 void set_last_error(const std::string& msg);
 
@@ -206,6 +234,18 @@ cudaError_t launch_dcp_split(int R, int I, int T, int K, const int32_t* sel, con
                              int32_t* status, cudaStream_t stream);
 cudaError_t launch_lse_combine(int R, int T, int H, const float* const* part_out, const float* const* part_lse,
                                float* out, float* lse, cudaStream_t stream);
+cudaError_t launch_paged_mla(const sml_problem& p, const uint16_t* q, const sml_cache& latent, const PagedSel& sel,
+                             uint16_t* out, float* lse, const PagedWs& ws, int32_t* status, cudaStream_t stream);
+cudaError_t launch_block_keys(const sml_cache& index, const int32_t* pages, int n, const sml_cache& block,
+                              int32_t* status, cudaStream_t stream);
+cudaError_t launch_block_scores(const sml_problem& p, const uint8_t* iq8, const float* iq_scale, const float* iw,
+                                const sml_cache& block, float* scores, int32_t* status, cudaStream_t stream);
+cudaError_t launch_block_topk(const sml_problem& p, const float* scores, int k, int32_t* blocks, int32_t* blocks_len,
+                              int32_t* status, cudaStream_t stream);
+cudaError_t launch_latent_read(const int32_t* slot, int n, const sml_cache& cache, void* c, void* kpe,
+                               int32_t* status, cudaStream_t stream);
+cudaError_t launch_indexer_k_read(const int32_t* slot, int n, const sml_cache& cache, void* k, int32_t* status,
+                                  cudaStream_t stream);
 cudaError_t launch_indexer_q_quant(const void* iq, int T, void* iq8, float* iq_scale, cudaStream_t stream);
 
 }  // namespace sml

@@ -28,6 +28,18 @@ uint8)::
 reading the device arrays.  A shared-indexer layer passes the owner layer's
 idx / idx_len as reuse_idx / reuse_len; the stages run one by one through
 ``sml_indexer_scores``, ``sml_topk`` and ``sml_sparse_mla_decode``.
+
+A layer that attends to the whole cache (or its last ``window`` tokens), and one
+that attends to the pages a block score selects (``block_pool``: one key per page of
+the indexer pool; ``ws`` of SML_STAGE_PAGED bytes; ``out16`` bf16)::
+
+    sml.sml_paged_mla_decode(p, q, latent_pool, out16, lse, ws)
+    sml.sml_block_keys_write(index_pool, filled_pages, block_pool, ws)   # pages that just filled
+    sml.sml_block_scores(p, iq8, iq_scale, iw, block_pool, block_scores, ws)
+    sml.sml_block_topk(p, block_scores, blocks, blocks_len, ws)          # blocks [T, num_blocks]
+    sml.sml_block_mla_decode(p, q, latent_pool, blocks, blocks_len, out16, lse, ws)
+
+``sml_latent_cache_read`` and ``sml_indexer_k_cache_read`` give cached rows back as bf16.
 """
 from __future__ import annotations
 
@@ -60,6 +72,7 @@ SML_STAGE_INDEXER = 1
 SML_STAGE_TOPK = 2
 SML_STAGE_MLA = 3
 SML_STAGE_LAYER = 4
+SML_STAGE_PAGED = 5
 
 PAGE_TOKENS = 64
 LATENT_PAGE_BYTES = 64 * 656
@@ -154,6 +167,13 @@ def lib() -> ctypes.CDLL:
         L.sml_latent_cache_write.argtypes = [vp, vp, vp, ctypes.c_int32, Cache, vp, vp]
         L.sml_indexer_q_quant.argtypes = [vp, ctypes.c_int32, vp, vp, vp]
         i32p = ctypes.c_int32
+        L.sml_paged_mla_decode.argtypes = [pp, vp, Cache, i32p, vp, vp, vp, sz, vp]
+        L.sml_block_mla_decode.argtypes = [pp, vp, Cache, vp, vp, i32p, vp, vp, vp, sz, vp]
+        L.sml_block_keys_write.argtypes = [Cache, vp, i32p, Cache, vp, vp]
+        L.sml_block_scores.argtypes = [pp, vp, vp, vp, Cache, vp, vp, vp]
+        L.sml_block_topk.argtypes = [pp, vp, i32p, vp, vp, vp, vp]
+        L.sml_latent_cache_read.argtypes = [vp, i32p, Cache, vp, vp, vp, vp]
+        L.sml_indexer_k_cache_read.argtypes = [vp, i32p, Cache, vp, vp, vp]
         L.sml_dcp_merge_candidates.argtypes = [ctypes.POINTER(DcpRanks), i32p, i32p, vp, vp, vp, vp, vp]
         L.sml_dcp_pack_candidates.argtypes = [i32p, i32p, vp, ctypes.c_int64, vp, vp, vp, vp, vp]
         L.sml_dcp_split_selection.argtypes = [i32p, i32p, i32p, i32p, vp, vp, vp, ctypes.POINTER(vp),
@@ -167,7 +187,9 @@ def lib() -> ctypes.CDLL:
                      "sml_noalloc_read_status",
                      "sml_indexer_k_cache_write", "sml_latent_cache_write", "sml_indexer_q_quant",
                      "sml_dcp_merge_candidates", "sml_dcp_split_selection", "sml_lse_combine",
-                     "sml_dcp_pack_candidates"):
+                     "sml_dcp_pack_candidates", "sml_paged_mla_decode", "sml_block_mla_decode",
+                     "sml_block_keys_write", "sml_block_scores", "sml_block_topk", "sml_latent_cache_read",
+                     "sml_indexer_k_cache_read"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -311,6 +333,52 @@ def sml_latent_cache_write(c, k_pe, slot, latent, workspace=None, stream=None):
 def sml_indexer_q_quant(iq, iq8, iq_scale, stream=None):
     """Indexer queries iq [T, 64, 128] bf16 -> iq8 (e4m3 codes, uint8) and iq_scale [T] fp32."""
     _check(lib().sml_indexer_q_quant(_p(iq), _numel(iq_scale), _p(iq8), _p(iq_scale), _s(stream)))
+
+
+def sml_latent_cache_read(slot, latent, c, k_pe=None, workspace=None, stream=None):
+    """Cached latent rows slot [n] int32 as c [n, 512] bf16 (+ k_pe [n, 64] bf16, or None)."""
+    _check(lib().sml_latent_cache_read(_p(slot), _numel(slot), latent_cache(latent), _p(c), _p(k_pe),
+                                       _p(workspace), _s(stream)))
+
+
+def sml_indexer_k_cache_read(slot, index_cache, k, workspace=None, stream=None):
+    """Cached indexer keys slot [n] int32 as k [n, 128] bf16."""
+    _check(lib().sml_indexer_k_cache_read(_p(slot), _numel(slot), cache(index_cache, INDEX_PAGE_BYTES), _p(k),
+                                          _p(workspace), _s(stream)))
+
+
+def sml_paged_mla_decode(problem, q, latent, out, lse, workspace, window=0, stream=None):
+    """MLA over every visible cached token (window > 0: the last ``window`` of them):
+    out [T, H, 512] bf16, lse [T, H] fp32.  Workspace: SML_STAGE_PAGED."""
+    _check(lib().sml_paged_mla_decode(ctypes.byref(problem), _p(q), latent_cache(latent), window, _p(out), _p(lse),
+                                      _p(workspace), _nbytes(workspace), _s(stream)))
+
+
+def sml_block_mla_decode(problem, q, latent, blocks, blocks_len, out, lse, workspace, stream=None):
+    """MLA over the listed 64-token blocks, blocks [T, max_blocks] / blocks_len [T] int32:
+    out [T, H, 512] bf16, lse [T, H] fp32.  Workspace: SML_STAGE_PAGED."""
+    _check(lib().sml_block_mla_decode(ctypes.byref(problem), _p(q), latent_cache(latent), _p(blocks), _p(blocks_len),
+                                      blocks.shape[1], _p(out), _p(lse), _p(workspace), _nbytes(workspace),
+                                      _s(stream)))
+
+
+def sml_block_keys_write(index_cache, pages, block_cache, workspace=None, stream=None):
+    """Mean key of every listed physical page [n] int32 of the indexer cache into the
+    block pool (indexer layout, row = page)."""
+    _check(lib().sml_block_keys_write(cache(index_cache, INDEX_PAGE_BYTES), _p(pages), _numel(pages),
+                                      cache(block_cache, INDEX_PAGE_BYTES), _p(workspace), _s(stream)))
+
+
+def sml_block_scores(problem, iq8, iq_scale, iw, block_cache, scores, workspace=None, stream=None):
+    """Indexer scores of the block keys: scores [T, max_pages] fp32."""
+    _check(lib().sml_block_scores(ctypes.byref(problem), _p(iq8), _p(iq_scale), _p(iw),
+                                  cache(block_cache, INDEX_PAGE_BYTES), _p(scores), _p(workspace), _s(stream)))
+
+
+def sml_block_topk(problem, scores, blocks, blocks_len, workspace=None, stream=None):
+    """The best blocks.shape[1] - 1 blocks of every token, ascending, then its newest block."""
+    _check(lib().sml_block_topk(ctypes.byref(problem), _p(scores), blocks.shape[1], _p(blocks), _p(blocks_len),
+                                _p(workspace), _s(stream)))
 
 
 def _ptrs(tensors):

@@ -1,0 +1,71 @@
+"""Inputs, expected values and error bounds shared by the tests of the whole-cache operators.
+
+Bounds of the attention's outputs, from its arithmetic (u = 2^-8, half a bf16 step relative
+to the value):
+
+* the output is rounded to bf16 once: u |out|;
+* each softmax weight has at least 8 significant bits when it enters its product (u relative,
+  plus 2^-11 for one rounding to half precision on the way); the same weights unrounded are
+  summed for the denominator, so an output is off by at most (u + 2^-11) A, A = sum_i p_i |c_i|;
+* a weight far below the largest keeps only an absolute error: half of E4M3's subnormal step
+  (2^-10) against a largest weight-times-scale of at least 28 (an output's keys share it within
+  the spread of their block scales, a factor 4 for these inputs): 2^-10 / 28 * 4 <= 2^-12.8 of
+  the largest p, times sum_i |c_i|;
+* a logit is a sum in fp32 of up to 576 products: off by at most d = 576 * 2^-23 of the summed terms'
+  size (2^-23, not 2^-24: the tensor cores may cut instead of round).  A softmax weight then moves by
+  p_i |d_i - mean d| <= 2 d p_i (1 - p_i), the output by 2 d sum_i p_i (1 - p_i) |c_i|, and the
+  log-sum-exp by d, plus 2^-20 (1 + |lse|) for log2, exp2 and the sum of the weights.
+"""
+import numpy as np
+
+from oracle import dsa, formats as F, mla
+from tests import parity
+
+U = 2.0 ** -8
+
+
+def expect(wl, layer_i, t, positions, n=None, nss=None):
+    """(out, lse, out bound, lse bound) of token t over logical positions, in float64."""
+    v = wl.view(layer_i)
+    r = int(dsa.request_of_tokens(wl.cu_q)[t])
+    if n is None:
+        n = int(dsa.visible_lengths(wl.cu_q, wl.ctx_len)[t])
+    q = F.decode_bf16(v.q[t])
+    H = q.shape[0]
+    if len(positions) == 0:
+        return np.zeros((H, 512)), np.full(H, -np.inf), np.zeros((H, 512)), np.zeros(H)
+    pages, rows = F.physical(wl.block_table[r], positions)
+    c, k_pe = F.latent_rows(parity.oracle_latent(wl), pages, rows)
+    scale = wl.sm_scale * dsa.ssmax_factor(wl.ssmax, wl.ssmax_s, n if nss is None else nss)
+    out, lse = mla.attend(q, c, k_pe, v.rope_dim, scale)
+    keys = np.concatenate([c, k_pe], 1)[:, :q.shape[1]]
+    p = np.exp(scale * (q @ keys.T) - lse[:, None])
+    A = p @ np.abs(c)
+    d = 576 * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(keys).T).max(1)
+    tol = 2 * d[:, None] * ((p * (1 - p)) @ np.abs(c)) + U * np.abs(out) + (U + 2.0 ** -11) * A * 1.01 + 2.0 ** -12.8 * p.max(1)[:, None] * np.abs(c).sum(0)[None]
+    return out, lse, tol, d + 2.0 ** -20 * (1 + np.abs(lse))
+
+
+def check(name, got_out, got_lse, want):
+    out, lse, tol, ltol = want
+    got_out, got_lse = got_out.astype(np.float64), got_lse.astype(np.float64)
+    assert np.isfinite(got_out).all(), name
+    assert np.array_equal(np.isfinite(got_lse), np.isfinite(lse)), f"{name}: finiteness of lse"
+    over = np.abs(got_out - out) - tol
+    assert (over <= 0).all(), f"{name}: out off by up to {np.abs(got_out - out).max():.3e}, {(over > 0).sum()} beyond"
+    fin = np.isfinite(lse)
+    d = np.abs(got_lse[fin] - lse[fin])
+    assert (d <= ltol[fin]).all(), f"{name}: lse off by {d.max():.3e}, allowed {ltol[fin].min():.3e}"
+
+
+def spoil_unused(wl, positions_kept=None):
+    """NaN codes, NaN scales and NaN RoPE keys (0xFF bytes) in every row of the pool that no
+    request holds, the rows behind each request's last token among them."""
+    row = {"e4m3": 576, "bf16": 1152}.get(wl.latent_format, 656)
+    lat = wl.latent.reshape(wl.num_pages * 64, row)
+    held = np.zeros(wl.num_pages * 64, dtype=bool)
+    for r in range(wl.B):
+        pos = np.arange(int(wl.ctx_len[r]))
+        held[wl.block_table[r, pos // 64].astype(np.int64) * 64 + pos % 64] = True
+    lat[~held] = 0xFF
+    return wl
