@@ -517,18 +517,6 @@ indexer_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 // Encoded tensor maps depend only on the address, the shape and the device:
 // the last few are kept so that a call with the same caches and batch shape
 // (every decode step) does not re-encode them.
@@ -570,10 +558,22 @@ cudaError_t launch_cfg(const CUtensorMap& kmap, const CUtensorMap& qmap, const P
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
 cudaError_t launch_indexer(const sml_problem& p, const uint8_t* iq8, const float* iq_scale,
                            const float* iw, const uint8_t* index_base, int64_t index_pages,
                            float* scores, int32_t* status, cudaStream_t stream) {
-  auto enc = encode_fn();
+  auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   CUtensorMap kmap, qmap;
   static MapCache kcache, qcache;

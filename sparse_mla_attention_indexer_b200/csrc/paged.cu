@@ -10,6 +10,7 @@
 // over the positions i that the token attends to, in one pass over the rows
 // with a running maximum and sum per head.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -19,12 +20,21 @@
 namespace sml {
 namespace {
 
-constexpr int kHU = 16;            // heads per unit
-constexpr int kThreads = 256;
-constexpr int kMaxThreads = 1024;
-constexpr int kRowF = 577;         // floats per staged row (odd: no bank conflicts)
+constexpr int kKT = 128;                 // keys per tile: two pages
+constexpr int kLatBlock = kKT * 128;     // one 128-B wide block of a tile
+constexpr int kSoftmaxWarps = 16;        // warps 0-15
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kWarpMma = 16, kWarpLoad = 17;
+constexpr int kThreads = 576;
+constexpr uint32_t kColO = 256;          // TMEM: logits from column 0, O from here
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Weight exponents: a weight is capped at 440 (E4M3's largest value is 448;
+// the margin covers the approximate 2^x and log2).
+constexpr float kLog2Cap = 8.78135971f;    // log2(440)
+constexpr float kLog2Head = 6.80735492f;   // log2(112)
+template <int kHU>
+constexpr int kGroupBf = 2 * kHU * 2 * 8;  // bytes of an 8-key group of bf16 weights
 
 struct Params {
   int B, T, H, rope_dim, max_ctx, max_pages, ssmax;
@@ -35,9 +45,7 @@ struct Params {
   const int32_t* vis_len;
   const int32_t* ssmax_len;
   const uint16_t* q;
-  const uint8_t* latent;
   int64_t latent_pages;
-  int format;
   float latent_scale;
   PagedSel sel;
   uint16_t* out;
@@ -113,7 +121,7 @@ struct Range {
   int used, t0;
 };
 struct PlanSmem {
-  long long part[kMaxThreads / 32];
+  long long part[kThreads / 32];
   long long tok0;
   int t0;
 };
@@ -166,38 +174,294 @@ __device__ Range plan_range(const Params& P, int gi, PlanSmem& S) {
   return R;
 }
 
-__device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ float e4m3_f(uint8_t v) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)v, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
-}
+// ---- the attention kernel -------------------------------------------------------
 
-// Value d of the row at `row` (512 latent values, then 64 RoPE values).
-__device__ __forceinline__ float row_value(const Params& P, const uint8_t* row, int d) {
-  if (P.format == SML_LATENT_BF16) return bf16_f(reinterpret_cast<const uint16_t*>(row)[d]);
-  if (P.format == SML_LATENT_E4M3) return e4m3_f(row[d]) * P.latent_scale;
-  if (d < SML_LATENT_DIM) return e4m3_f(row[d]) * reinterpret_cast<const float*>(row + SML_LATENT_DIM)[d >> 7];
-  return bf16_f(reinterpret_cast<const uint16_t*>(row + SML_LATENT_DIM + 16)[d - SML_LATENT_DIM]);
-}
+// Latent formats of the kernel's template parameter.
+constexpr int kFmtDsMla = SML_LATENT_FP8_DS_MLA, kFmtPlain = SML_LATENT_E4M3, kFmtBf16 = SML_LATENT_BF16;
+template <int kFmt>
+struct Fmt {
+  static constexpr bool kDs = kFmt == kFmtDsMla, kPlain = kFmt == kFmtPlain, kBf = kFmt == kFmtBf16;
+  static constexpr int kBufs = kBf ? 1 : 2;        // tile buffers (a bf16 tile is 144 KB)
+  static constexpr int kBlocks = kBf ? 8 : 4;      // 128-B wide blocks of a tile's latents
+  static constexpr int kSets = kDs ? 4 : 1;        // weight sets: one per block scale
+  static constexpr int kPeX = kBf ? 2 * SML_LATENT_DIM : kPlain ? SML_LATENT_DIM : SML_LATENT_DIM + 16;
+};
 
-struct Smem {
-  float row[SML_PAGE_TOKENS][kRowF];
-  float q[kHU][kRowF];
-  float p[kHU][SML_PAGE_TOKENS];
-  float fac[kHU];
+template <int kFmt, int kHU>
+struct __align__(1024) Smem {
+  using F = Fmt<kFmt>;
+  static constexpr int kSetBytes = kKT * 2 * kHU * (F::kBf ? 2 : 1);   // both terms of one weight set
+  // With 32 heads per unit the last two weight sets of a tile live where its
+  // RoPE keys were: those are dead once the tile's logits are done.
+  static constexpr bool kOverlay = F::kDs && kHU == 32;
+  static constexpr int kOwnSets = kOverlay ? 2 : F::kSets;
+  uint8_t lat[F::kBufs][F::kBlocks][kLatBlock];   // [buffer][block][128 keys x 128 B], SW128
+  uint8_t pe[F::kBufs][kKT * 128];                // [buffer][128 keys x 128 B] RoPE keys, SW128
+  uint8_t q8[1024 * kHU];   // E4M3: [block] 2 kHU rows (high, then low term) x 128 B, SW128; bf16: 8 blocks of kHU rows
+  uint8_t qpe[(F::kPlain ? 2 : 1) * kHU * 128];   // RoPE query, SW128 (plain E4M3: high, then low term)
+  uint8_t pb[kOwnSets][kSetBytes];                // weight sets: 8-key x 16-B core matrices
+  float sc[F::kDs ? F::kBufs : 1][kKT][4];        // [buffer][key] block scales
+  float xmax[4][4][kHU / 4];                      // [head quarter][key quarter][head]
+  float xscale[4][4][4];                          // [head quarter][key quarter][block]
+  float xsum[4][4][kHU / 4];
+  float qs[kHU];                                  // power-of-two query scale per head
+  int4 rows[4];                                   // [tile % 4] valid rows {lo, hi} of each page of the tile
+  uint64_t full[F::kBufs], lat_free[F::kBufs];
+  uint64_t q_ready, s_full, s_free, p_full, pv_done, o_free, drain;
+  uint32_t tmem_base;
+  int abort;
   PlanSmem plan;
 };
 
-__global__ void __launch_bounds__(kThreads) paged_mla_kernel(const Params P) {
-  extern __shared__ uint8_t raw[];
-  Smem& S = *reinterpret_cast<Smem*>(raw);
-  const int tid = threadIdx.x;
+// A piece of a token in this CTA's range: tiles [j0, j0 + ne) of it (ne = 0:
+// the token attends to nothing).
+struct Seg {
+  Tok tk;
+  int t, j0, ne;
+  bool whole;
+  size_t part;   // its first row in the partials
+};
+struct Walk {
+  long long u, ue;
+  int t, j0;
+};
+__device__ __forceinline__ bool walk_next(const Params& P, Walk& w, int slot, int heads, Seg& s) {
+  if (w.u >= w.ue) return false;
+  s.t = w.t;
+  s.tk = token_at(P, w.t);
+  const int nt = tiles_of(s.tk), nj = (int)min((long long)(nt - w.j0), w.ue - w.u);
+  s.j0 = w.j0;
+  s.ne = s.tk.np > 0 ? nj : 0;
+  s.whole = w.j0 == 0 && nj == nt;
+  s.part = (size_t)(slot + (w.j0 == 0)) * heads;
+  w.u += nj;
+  ++w.t;
+  w.j0 = 0;
+  return true;
+}
+
+// Cursor over the tiles of the range, in order: tile jj of the seg-th piece
+// that has any, the k-th tile overall.
+struct Cur {
+  Walk w;
+  int ne, jj, seg, k;
+  bool valid;
+};
+__device__ __forceinline__ void cur_seek(Cur& c, const Params& P) {
+  Seg s;
+  c.jj = 0;
+  c.valid = false;
+  while (walk_next(P, c.w, 0, 0, s)) {
+    c.ne = s.ne;
+    if (s.ne > 0) {
+      c.valid = true;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void cur_next(Cur& c, const Params& P) {
+  ++c.k;
+  if (++c.jj < c.ne) return;
+  ++c.seg;
+  cur_seek(c, P);
+}
+
+// Byte address of (row, 16-B chunk) in a 128-B-swizzled tile of 128-B rows.
+__device__ __forceinline__ uint32_t sw128(uint32_t base, int row, int chunk) {
+  return base + (row >> 3) * 1024 + (row & 7) * 128 + ((chunk ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void st_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_b32(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
+
+__device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
+}
+// Two floats -> E4M3 codes of the nearest values; x becomes the residuals.
+__device__ __forceinline__ uint32_t split_e4m3x2(float& x0, float& x1) {
+  const uint32_t c = f2_to_e4m3x2(x0, x1);
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
+  const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  x0 -= r.x;
+  x1 -= r.y;
+  return c;
+}
+// Two weights (each at most 448) as two E4M3 terms, hi + lo: eight significant
+// bits, as many as a bf16 has.  The residual is taken in half precision, where
+// both the rounded weight (2^-11) and the difference fit: three conversions
+// and one subtraction for two weights.
+__device__ __forceinline__ void split2_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 x = __floats2half2_rn(x0, x1);
+  const __half2_raw xr = *reinterpret_cast<const __half2_raw*>(&x);
+  hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(xr, __NV_SATFINITE, __NV_E4M3) & 0xffffu;
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
+  const __half2 r = __hsub2(x, *reinterpret_cast<const __half2*>(&b));
+  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
+}
+// AND of a flag over the softmax threads (named barrier 5): a wait that gave up
+// ends all of them together instead of leaving some blocked at a barrier.
+__device__ __forceinline__ bool softmax_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 5, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(kSoftmaxThreads)
+      : "memory");
+  return r != 0;
+}
+// OR of a flag over the four warps of one head quarter (named barrier 1 +
+// quarter; also a barrier for them).
+__device__ __forceinline__ bool group_any(int hq, bool v) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r)
+               : "r"((uint32_t)v), "r"(1 + hq)
+               : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int hq) { asm volatile("bar.sync %0, 128;" ::"r"(1 + hq) : "memory"); }
+
+__device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[4]) { ptx::tmem_ld4(a, r); }
+__device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[8]) { ptx::tmem_ld8(a, r); }
+__device__ __forceinline__ void tmem_stn(uint32_t a, const uint32_t (&r)[4]) { ptx::tmem_st4(a, r); }
+__device__ __forceinline__ void tmem_stn(uint32_t a, const uint32_t (&r)[8]) { ptx::tmem_st8(a, r); }
+
+// Stage the query of (token t, head group g); thread = head x 32-dim part of
+// 16.  E4M3 pools: q = s_h (hi + lo), both E4M3, s_h the power of two >= amax_h
+// / 448: exact wherever |q| >= 2^-6 s_h (a bf16 has 8 significant bits, four
+// in each term), else within 2^-10 s_h.  RoPE: bf16 as given (fp8_ds_mla), or
+// split the same way (plain E4M3).  bf16 pools: the bf16 query as given.
+template <int kFmt, int kHU>
+__device__ __forceinline__ void stage_query(const Params& P, Smem<kFmt, kHU>& S, int t, int g, int tid) {
+  using F = Fmt<kFmt>;
+  const int h = tid >> 4, p = tid & 15;
+  const uint16_t* qh = P.q + ((size_t)t * P.H + g * kHU + h) * (SML_LATENT_DIM + P.rope_dim);
+  const uint32_t q0 = ptx::smem_u32(S.q8), qp = ptx::smem_u32(S.qpe);
+  if constexpr (F::kBf) {
+    const int nc = P.rope_dim ? 72 : 64;
+    for (int c = p; c < nc; c += 16) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(qh) + c);
+      st_v4(c < 64 ? sw128(q0 + (c >> 3) * (kHU * 128), h, c & 7) : sw128(qp, h, c - 64), v.x, v.y, v.z, v.w);
+    }
+    if (p == 0) S.qs[h] = 1.f;
+  } else {
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const uint4*>(qh + 32 * p) + i);
+  uint2 pv = make_uint2(0u, 0u);
+  if (P.rope_dim) pv = __ldcg(reinterpret_cast<const uint2*>(qh + SML_LATENT_DIM + 4 * p));
+  auto amax2 = [](uint32_t w) { return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))); };
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    amax = fmaxf(amax, fmaxf(fmaxf(amax2(v[i].x), amax2(v[i].y)), fmaxf(amax2(v[i].z), amax2(v[i].w))));
+  if (F::kPlain) amax = fmaxf(amax, fmaxf(amax2(pv.x), amax2(pv.y)));
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  int e2 = 0;
+  if (amax > 0.f) frexpf(amax / 448.f, &e2);   // amax / 448 < 2^e2
+  const float inv = ldexpf(1.f, -e2);
+  if (p == 0) S.qs[h] = ldexpf(1.f, e2);
+  auto split4 = [&](uint32_t wa, uint32_t wb, uint32_t& hi, uint32_t& lo) {
+    float x0 = __uint_as_float(wa << 16) * inv, x1 = __uint_as_float(wa & 0xffff0000u) * inv;
+    float x2 = __uint_as_float(wb << 16) * inv, x3 = __uint_as_float(wb & 0xffff0000u) * inv;
+    hi = split_e4m3x2(x0, x1);
+    hi |= split_e4m3x2(x2, x3) << 16;
+    lo = f2_to_e4m3x2(x0, x1) | (f2_to_e4m3x2(x2, x3) << 16);
+  };
+  // dims [32 p, 32 p + 32) -> block p / 4, 16-B chunks 2 (p % 4) and 2 (p % 4) + 1
+  const uint32_t qb = q0 + (p >> 2) * (2 * kHU * 128);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t hw[4], lw[4];
+    split4(v[2 * c].x, v[2 * c].y, hw[0], lw[0]);
+    split4(v[2 * c].z, v[2 * c].w, hw[1], lw[1]);
+    split4(v[2 * c + 1].x, v[2 * c + 1].y, hw[2], lw[2]);
+    split4(v[2 * c + 1].z, v[2 * c + 1].w, hw[3], lw[3]);
+    const int chunk = 2 * (p & 3) + c;
+    st_v4(sw128(qb, h, chunk), hw[0], hw[1], hw[2], hw[3]);
+    st_v4(sw128(qb, h + kHU, chunk), lw[0], lw[1], lw[2], lw[3]);
+  }
+  if (P.rope_dim) {
+    if (F::kPlain) {
+      uint32_t hi, lo;
+      split4(pv.x, pv.y, hi, lo);
+      st_b32(sw128(qp, h, p >> 2) + 4 * (p & 3), hi);
+      st_b32(sw128(qp, h + kHU, p >> 2) + 4 * (p & 3), lo);
+    } else {
+      st_v2(sw128(qp, h, p >> 1) + 8 * (p & 1), pv.x, pv.y);
+    }
+  }
+  }
+}
+
+template <int kFmt, int kHU>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant__ CUtensorMap scale_map,
+                 const __grid_constant__ Params P) {
+  using F = Fmt<kFmt>;
+  using Sm = Smem<kFmt, kHU>;
+  constexpr int kBufs = F::kBufs, kHT = kHU / 4;   // kHT: heads per softmax thread
+  extern __shared__ uint8_t smem_raw[];
+  Sm& S = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = (int)blockIdx.x % P.ws.hg, gi = (int)blockIdx.x / P.ws.hg;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBufs; ++i) {
+      ptx::mbar_init(&S.full[i], 1);
+      ptx::mbar_init(&S.lat_free[i], 1);
+    }
+    ptx::mbar_init(&S.q_ready, 16 * kHU / 32);
+    ptx::mbar_init(&S.s_full, 1);
+    ptx::mbar_init(&S.s_free, kSoftmaxWarps);
+    ptx::mbar_init(&S.p_full, kSoftmaxWarps);
+    ptx::mbar_init(&S.pv_done, 1);
+    ptx::mbar_init(&S.o_free, kSoftmaxWarps);
+    ptx::mbar_init(&S.drain, 1);
+    S.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    ptx::tmem_alloc(&S.tmem_base, 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == kWarpLoad && lane == 0) {
+    ptx::prefetch_tensormap(&row_map);
+    if (F::kDs) ptx::prefetch_tensormap(&scale_map);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
   ptx::griddep_wait();
-  if (tid == 0) ptx::griddep_launch_dependents();
+  // this CTA holds its tensor memory: a dependent grid cannot starve it
+  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+  volatile int* abort = &S.abort;
+  const uint32_t T0 = S.tmem_base;
   const Range R = plan_range<kThreads>(P, gi, S.plan);
   const int slot = (g * P.ws.cpg + gi) * 2;
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     // the token to join at this CTA: the one it continues, if the CTA before began it
     int4 rec = make_int4(-1, 0, 0, 0);
     if (gi < R.used && R.ub > R.tok0) {
@@ -207,116 +471,511 @@ __global__ void __launch_bounds__(kThreads) paged_mla_kernel(const Params P) {
     }
     P.ws.join[g * P.ws.cpg + gi] = rec;
   }
-  const int D = SML_LATENT_DIM + P.rope_dim, rowb = P.format == SML_LATENT_BF16  ? SML_LATENT_BF16_ROW_BYTES
-                                                     : P.format == SML_LATENT_E4M3 ? SML_LATENT_E4M3_ROW_BYTES
-                                                                                   : SML_LATENT_ROW_BYTES;
-  long long u = R.ub;
-  int j0 = (int)(R.ub - R.tok0);
-  for (int t = R.t0; u < R.ue; ++t, j0 = 0) {
-    const Tok tk = token_at(P, t);
-    const int nt = tiles_of(tk), j1 = (int)min((long long)nt, j0 + (R.ue - u));
-    u += j1 - j0;
-    if (tid == 0) {
-      if (!tk.ok) raise_fault(P.status, SML_FAULT_LENGTHS);
-      if (tk.len_bad) raise_fault(P.status, SML_FAULT_TOPK_LEN);
+  const Walk begin = {R.ub, R.ue, R.t0, (int)(R.ub - R.tok0)};
+
+  if (warp == kWarpLoad) {
+    // ================= producer: page ids, then TMA =================
+    Walk w = begin;
+    Seg s;
+    int k = 0;   // tiles so far
+    bool ok = true;
+    const bool rope = P.rope_dim != 0;
+    constexpr uint32_t kPageBytes = F::kBlocks * SML_PAGE_TOKENS * 128 + (F::kDs ? SML_PAGE_TOKENS * 16 : 0);
+    const uint32_t page_bytes = kPageBytes + (rope ? SML_PAGE_TOKENS * 128 : 0);
+    while (ok && walk_next(P, w, slot, kHU, s)) {
+      if (lane == 0 && g == 0) {
+        if (!s.tk.ok) raise_fault(P.status, SML_FAULT_LENGTHS);
+        if (s.tk.len_bad) raise_fault(P.status, SML_FAULT_TOPK_LEN);
+      }
+      int ph = -1, lg = 0;   // of page 2 (j0 + 16 i) + lane
+      for (int jj = 0; jj < s.ne; ++jj, ++k) {
+        const int buf = k % kBufs, two = 2 * (jj & 15);
+        if (two == 0) ph = page_at(P, s.tk, s.t, 2 * (s.j0 + jj) + lane, lane < 2 * (s.ne - jj), &lg);
+        const int p0 = __shfl_sync(0xffffffffu, ph, two), p1 = __shfl_sync(0xffffffffu, ph, two + 1);
+        const int l0 = __shfl_sync(0xffffffffu, lg, two), l1 = __shfl_sync(0xffffffffu, lg, two + 1);
+        if (k >= kBufs) ok = warp_wait(&S.lat_free[buf], ((k / kBufs) - 1) & 1, abort);
+        if (!ok) break;
+        if (lane == 0) {
+          int4 r;   // valid rows of each page: none of one that is not loaded
+          r.x = max(0, s.tk.lo - l0 * SML_PAGE_TOKENS);
+          r.y = p0 >= 0 ? min(SML_PAGE_TOKENS, s.tk.n - l0 * SML_PAGE_TOKENS) : 0;
+          r.z = max(0, s.tk.lo - l1 * SML_PAGE_TOKENS);
+          r.w = p1 >= 0 ? min(SML_PAGE_TOKENS, s.tk.n - l1 * SML_PAGE_TOKENS) : 0;
+          S.rows[k & 3] = r;   // last read by the softmax of tile k - 4
+          ptx::mbar_arrive_expect_tx(&S.full[buf], ((p0 >= 0) + (p1 >= 0)) * page_bytes);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const int pg = half ? p1 : p0;
+            if (pg < 0) continue;
+            const int y = pg * SML_PAGE_TOKENS, off = half * SML_PAGE_TOKENS * 128;
+            // what the logits wait for first: scales and RoPE are small
+            if (F::kDs) ptx::tma_load_2d(&S.sc[F::kDs ? buf : 0][half * SML_PAGE_TOKENS][0], &scale_map, &S.full[buf], SML_LATENT_DIM, y);
+#pragma unroll
+            for (int b = 0; b < F::kBlocks; ++b)
+              ptx::tma_load_2d(S.lat[buf][b] + off, &row_map, &S.full[buf], 128 * b, y);
+            if (rope) ptx::tma_load_2d(S.pe[buf] + off, &row_map, &S.full[buf], F::kPeX, y);
+          }
+        }
+        __syncwarp();
+      }
     }
-    __syncthreads();
-    for (int i = tid; i < kHU * D; i += kThreads)
-      S.q[i / D][i % D] = bf16_f(P.q[((size_t)t * P.H + g * kHU + i / D) * D + i % D]);
-    const float zscale = P.sm_scale * (P.ssmax ? P.ssmax_s * logf((float)tk.nss) : 1.f) * kLog2e;
-    float m = -INFINITY, l = 0.f, acc[2][kHU];
+    if (!ok) *abort = 1;
+    // nothing of this CTA's in flight when its shared memory goes away
+    for (int i = max(0, k - kBufs); i < k; ++i) ptx::mbar_wait(&S.full[i % kBufs], (i / kBufs) & 1, nullptr, 100000u);
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // ================= MMA issuer =================
+    const uint32_t id_qk = F::kBf ? ptx::idesc_f16(kHU, 1, 0, 0) : ptx::idesc_f16(kHU, 0, 0, 0);
+    const uint32_t id_pe = ptx::idesc_f16(kHU, 1, 0, 0);
+    const uint32_t id_pv = F::kBf ? ptx::idesc_f16(2 * kHU, 1, 1, 1) : ptx::idesc_f16(2 * kHU, 0, 1, 1);
+    const uint32_t q0 = ptx::smem_u32(S.q8), qp = ptx::smem_u32(S.qpe);
+    auto issue_qk = [&](int buf) {
+      const uint32_t pe0 = ptx::smem_u32(S.pe[buf]);
+      if constexpr (F::kBf) {
+        // S^T = C . Q^T + K_pe . Q_pe^T, 16 dims per step
 #pragma unroll
-    for (int h = 0; h < kHU; ++h) acc[0][h] = acc[1][h] = 0.f;
-    for (int k = 2 * j0; k < min(tk.np, 2 * j1); ++k) {
-      int lg;
-      const int ph = page_at(P, tk, t, k, tid == 0, &lg);
-      if (ph < 0) continue;
-      __syncthreads();
-      const int lo = max(0, tk.lo - lg * SML_PAGE_TOKENS), hi = min(SML_PAGE_TOKENS, tk.n - lg * SML_PAGE_TOKENS);
-      for (int i = tid; i < SML_PAGE_TOKENS * D; i += kThreads) {
-        const int row = i / D, d = i % D;
-        S.row[row][d] =
-            row >= lo && row < hi ? row_value(P, P.latent + ((size_t)ph * SML_PAGE_TOKENS + row) * rowb, d) : 0.f;
-      }
-      __syncthreads();
-      // thread = (head, keys kk, kk + 16, ...)
-      const int h = tid >> 4, kk = tid & 15;
-      float z[4], mt = m;
+        for (int b = 0; b < 8; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = kk + 16 * i;
-        float s = 0.f;
-        for (int d = 0; d < D; ++d) s = fmaf(S.q[h][d], S.row[key][d], s);
-        z[i] = key >= lo && key < hi ? s * zscale : -INFINITY;
-        mt = fmaxf(mt, z[i]);
-      }
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_ss(T0, ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
+                            ptx::sdesc_sw128(q0 + b * (kHU * 128) + 32 * kk), id_qk, (b | kk) != 0);
+        if (P.rope_dim) {
 #pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mt);
-      l *= f;
-      m = mt;
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_ss(T0, ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk), id_qk, 1);
+        }
+      } else {
+        // S_b^T = C_b . (Qhi_b + Qlo_b)^T, 32 dims per step (plain E4M3: one sum over the blocks)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = z[i] == -INFINITY ? 0.f : exp2f(z[i] - m);
-        l += p;
-        S.p[h][kk + 16 * i] = p;
-      }
-      if (kk == 0) S.fac[h] = f;
-      __syncthreads();
+        for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int hh = 0; hh < kHU; ++hh) {
-        acc[0][hh] *= S.fac[hh];
-        acc[1][hh] *= S.fac[hh];
-      }
-      for (int key = 0; key < SML_PAGE_TOKENS; ++key) {
-        const float v0 = S.row[key][tid], v1 = S.row[key][tid + kThreads];
+          for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int hh = 0; hh < kHU; ++hh) {
-          acc[0][hh] = fmaf(S.p[hh][key], v0, acc[0][hh]);
-          acc[1][hh] = fmaf(S.p[hh][key], v1, acc[1][hh]);
+            for (int term = 0; term < 2; ++term)
+              ptx::mma_f8f6f4_ss(T0 + (F::kDs ? kHU * b : 0), ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
+                                 ptx::sdesc_sw128(q0 + (2 * b + term) * (kHU * 128) + 32 * kk), id_qk,
+                                 F::kDs ? (kk | term) != 0 : (kk | b | term) != 0);
+        if (P.rope_dim) {
+          if (F::kDs) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::mma_f16_ss(T0 + 4 * kHU, ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk), id_pe, kk > 0);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+              for (int term = 0; term < 2; ++term)
+                ptx::mma_f8f6f4_ss(T0, ptx::sdesc_sw128(pe0 + 32 * kk),
+                                   ptx::sdesc_sw128(qp + term * (kHU * 128) + 32 * kk), id_qk, 1);
+          }
         }
       }
-    }
+      ptx::mma_commit(&S.s_full);
+    };
+    // O_b^T (+)= C_b^T . [Bhi_b; Blo_b]^T.  A: the tile read MN-major (dims
+    // contiguous; 8-key swizzle atoms 1,024 B apart; of a bf16 tile the two
+    // 64-dim atoms of an output block 16 KB apart).  B: 8-key x 16-B core
+    // matrices, along the heads 128 B apart.
+    constexpr int kKeysPerStep = F::kBf ? 16 : 32;
+    constexpr uint32_t kGroup = 2 * kHU * (F::kBf ? 2 : 1) * 8;   // bytes of an 8-key group of a weight set
+    auto issue_pv = [&](int buf, bool first) {
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    __syncthreads();
-    const bool whole = j0 == 0 && j1 == nt;
-    const size_t prow = (size_t)(slot + (j0 == 0)) * kHU;
-    if ((tid & 15) == 0) {
-      const int h = tid >> 4;
-      S.fac[h] = l > 0.f ? 1.f / l : 0.f;
-      const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-      if (whole) P.lse[(size_t)t * P.H + g * kHU + h] = lse;
-      else P.ws.part_lse[prow + h] = lse;
-    }
-    __syncthreads();
+      for (int st = 0; st < kKT / kKeysPerStep; ++st)
 #pragma unroll
-    for (int h = 0; h < kHU; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float o = acc[i][h] * S.fac[h];
-        const int d = tid + i * kThreads;
-        if (whole) {
-          const __nv_bfloat16 b = __float2bfloat16_rn(o);
-          P.out[((size_t)t * P.H + g * kHU + h) * SML_LATENT_DIM + d] = *reinterpret_cast<const uint16_t*>(&b);
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t set = F::kSets == 1 ? ptx::smem_u32(S.pb[0])
+                               : Sm::kOverlay && b >= 2 ? ptx::smem_u32(S.pe[buf]) + (b - 2) * Sm::kSetBytes
+                                                        : ptx::smem_u32(S.pb[Sm::kOverlay ? b & 1 : b]);
+          const uint64_t bd = ptx::sdesc(set + st * (kKeysPerStep / 8) * kGroup, kGroup, 128, 0);
+          const uint32_t d = T0 + kColO + 2 * kHU * b;
+          if constexpr (F::kBf)
+            ptx::mma_f16_ss(d, ptx::sdesc(ptx::smem_u32(S.lat[buf][2 * b]) + 2048 * st, 16384, 1024, 2), bd, id_pv, !first || st > 0);
+          else
+            ptx::mma_f8f6f4_ss(d, ptx::sdesc(ptx::smem_u32(S.lat[buf][b]) + 4096 * st, 16384, 1024, 2), bd, id_pv, !first || st > 0);
+        }
+      ptx::mma_commit(&S.pv_done);
+      ptx::mma_commit(&S.lat_free[buf]);
+    };
+    // The next QK^T and the next PV: whichever is ready goes first, QK^T at
+    // most one tile ahead.  A tile's QK^T needs its rows, the last S read and,
+    // for the first tile of a piece, the staged query; its PV needs its weights
+    // and, for the first tile of a later piece, the last O read.
+    Cur cq;
+    cq.w = begin;
+    cq.seg = cq.k = 0;
+    cur_seek(cq, P);
+    Cur cv = cq;
+    bool ok = true;
+    uint32_t idle = 0;
+    while (ok && cv.valid) {
+      int act = 0;   // 1: PV of cv, 2: QK^T of cq, -1: gave up
+      if (lane == 0) {
+        const bool pv_first = cv.jj == 0 && cv.seg > 0;
+        if (cv.k < cq.k && ptx::mbar_test_wait(&S.p_full, cv.k & 1) &&
+            (!pv_first || ptx::mbar_test_wait(&S.o_free, (cv.seg - 1) & 1))) {
+          act = 1;
+        } else if (cq.valid && cq.k <= cv.k + 1 && (cq.jj > 0 || ptx::mbar_test_wait(&S.q_ready, cq.seg & 1)) &&
+                   ptx::mbar_test_wait(&S.full[cq.k % kBufs], (cq.k / kBufs) & 1) &&
+                   (cq.k == 0 || ptx::mbar_test_wait(&S.s_free, (cq.k - 1) & 1))) {
+          act = 2;
+        } else if (*abort || ++idle > (1u << 22)) {
+          act = -1;
         } else {
-          P.ws.part_out[(prow + h) * SML_LATENT_DIM + d] = o;
+          // sleep on the barrier the next step most likely waits for
+          if (cv.k < cq.k) ptx::mbar_try_wait_ns(&S.p_full, cv.k & 1, 200);
+          else if (cq.valid) ptx::mbar_try_wait_ns(&S.full[cq.k % kBufs], (cq.k / kBufs) & 1, 200);
+        }
+        if (act == 1) {
+          ptx::tc_fence_after();
+          issue_pv(cv.k % kBufs, cv.jj == 0);
+        } else if (act == 2) {
+          ptx::tc_fence_after();
+          issue_qk(cq.k % kBufs);
         }
       }
+      act = __shfl_sync(0xffffffffu, act, 0);
+      if (act == 1) {
+        cur_next(cv, P);
+        idle = 0;
+      } else if (act == 2) {
+        cur_next(cq, P);
+        idle = 0;
+      } else if (act < 0) {
+        ok = false;
+      }
+    }
+    if (lane == 0) {
+      if (!ok) *abort = 1;
+      // every MMA this thread issued has finished before TMEM is released
+      ptx::mma_commit(&S.drain);
+      ptx::mbar_wait(&S.drain, 0, nullptr, 100000u);
+    }
+    __syncwarp();
+  } else if (warp < kSoftmaxWarps) {
+    // ================= softmax =================
+    // TMEM lane quarter (keys, and latent dims in the epilogue) and head
+    // quarter: this thread owns key (or dim) `row` for heads kHT hq ..
+    const int q4 = warp & 3, hq = warp >> 2, row = 32 * q4 + lane, tid = threadIdx.x;
+    const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+    constexpr int kStageWarps = 16 * kHU / 32;
+    auto stage = [&](const Seg& s) {
+      if (warp < kStageWarps) {
+        stage_query<kFmt, kHU>(P, S, s.t, g, tid);
+        ptx::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.q_ready);
+      }
+    };
+    Walk w = begin;
+    Seg s;
+    int k = 0;
+    bool ok = true, staged = false;
+    while (walk_next(P, w, slot, kHU, s)) {
+      // every softmax thread is done with the last piece: its S.qs and S.xsum
+      ok = softmax_all(ok);
+      if (!ok) break;
+      const size_t orow = (size_t)s.t * P.H + g * kHU;
+      if (s.ne == 0) {
+        // nothing to attend to (always a whole token)
+        for (int i = tid; i < kHU * SML_LATENT_DIM / 8; i += kSoftmaxThreads)
+          reinterpret_cast<uint4*>(P.out + orow * SML_LATENT_DIM)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid < kHU) P.lse[orow + tid] = -INFINITY;
+        continue;
+      }
+      if (!staged) stage(s);
+      staged = false;
+      ok = softmax_all(ok);   // S.qs visible to every softmax thread
+      // logits in log2 units, so that p = 2^(z - M)
+      const float zscale = P.sm_scale * (P.ssmax ? P.ssmax_s * logf((float)s.tk.nss) : 1.f) * kLog2e *
+                           (F::kPlain ? P.latent_scale : 1.f);
+      float qsh[kHT], M[kHT], lrow[kHT];
+#pragma unroll
+      for (int h = 0; h < kHT; ++h) {
+        qsh[h] = S.qs[kHT * hq + h];
+        M[h] = -INFINITY;
+        lrow[h] = 0.f;
+      }
+      // Block scales enter the weights relative to 2^eb, the largest of the
+      // block in the piece's first tile, so that blocks of different magnitude
+      // all use E4M3's range; the output is multiplied back.
+      float ebf[4] = {1.f, 1.f, 1.f, 1.f}, ebi[4] = {1.f, 1.f, 1.f, 1.f};
+      for (int jj = 0; jj < s.ne; ++jj, ++k) {
+        const int buf = k % kBufs;
+        ok = ok && warp_wait(&S.full[buf], (k / kBufs) & 1, abort) && warp_wait(&S.s_full, k & 1, abort);
+        if (!ok) *abort = 1;
+        ok = softmax_all(ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const int4 rr = S.rows[k & 3];
+        const int prow = row & 63;
+        const bool valid = row < 64 ? prow >= rr.x && prow < rr.y : prow >= rr.z && prow < rr.w;
+        float scv[4] = {1.f, 1.f, 1.f, 1.f};
+        float z[kHT];
+        if constexpr (F::kDs) {
+          const float4 f = *reinterpret_cast<const float4*>(S.sc[buf][row]);
+          scv[0] = valid ? f.x : 0.f;
+          scv[1] = valid ? f.y : 0.f;
+          scv[2] = valid ? f.z : 0.f;
+          scv[3] = valid ? f.w : 0.f;
+          uint32_t v[5][kHT];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tmem_ldn(T0 + kHU * b + kHT * hq + lane_off, v[b]);
+          if (P.rope_dim) tmem_ldn(T0 + kHU * 4 + kHT * hq + lane_off, v[4]);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int b = 0; b < 4; ++b) ptx::reg_fence(v[b]);
+          if (P.rope_dim) ptx::reg_fence(v[4]);
+#pragma unroll
+          for (int h = 0; h < kHT; ++h) {
+            z[h] = 0.f;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) z[h] = fmaf(scv[b], __uint_as_float(v[b][h]), z[h]);
+            z[h] *= qsh[h];
+            if (P.rope_dim) z[h] += __uint_as_float(v[4][h]);
+          }
+        } else {
+          uint32_t v[kHT];
+          tmem_ldn(T0 + kHT * hq + lane_off, v);
+          ptx::tmem_wait_ld(v);
+#pragma unroll
+          for (int h = 0; h < kHT; ++h) z[h] = __uint_as_float(v[h]) * qsh[h];
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.s_free);   // S read: the next tile's QK^T may overwrite it
+#pragma unroll
+        for (int h = 0; h < kHT; ++h) z[h] = valid ? z[h] * zscale : -INFINITY;
+        if (F::kDs && jj == 0) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const float x = ptx::warp_max_f32(scv[b]);
+            if (lane == 0) S.xscale[hq][q4][b] = x;
+          }
+          group_sync(hq);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const float x = fmaxf(fmaxf(S.xscale[hq][0][b], S.xscale[hq][1][b]), fmaxf(S.xscale[hq][2][b], S.xscale[hq][3][b]));
+            const int e = min(max((int)((__float_as_uint(x) >> 23) & 255) - 127, -100), 100);
+            ebf[b] = __int_as_float((127 - e) << 23);
+            ebi[b] = __int_as_float((127 + e) << 23);
+          }
+        }
+        // This key's weights 2^(z - M_h) scale_b must stay within E4M3's 448.
+        // A weight above the cap, or a head without M_h yet, sends the
+        // quarter's four warps through the exact update (a vote: rare after
+        // the first tile).  bf16: no scales; M_h only keeps 2^(z - M_h) within
+        // 2^16.
+        float lk = 0.f;
+        if constexpr (F::kDs) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) scv[b] *= ebf[b];
+          lk = lg2(fmaxf(fmaxf(fmaxf(scv[0], scv[1]), fmaxf(scv[2], scv[3])), 0x1p-60f));
+        }
+        constexpr float kCap = F::kBf ? 16.f : kLog2Cap, kHead = F::kBf ? 0.f : kLog2Head;
+        bool need = false;
+#pragma unroll
+        for (int h = 0; h < kHT; ++h) need = need || (z[h] != -INFINITY && !(z[h] - M[h] + lk <= kCap));
+        need = group_any(hq, need);
+        float f[kHT];
+        bool any = false;
+        if (need) {
+          // A head whose largest weight of this tile passes the cap takes the
+          // integer M_h that puts it in (56, 112]: headroom of 4 for later
+          // tiles, and the dominant weights keep all eight bits.  O and the
+          // row sums scale by 2^(M_old - M_new), exactly.
+#pragma unroll
+          for (int h = 0; h < kHT; ++h) {
+            const float x = ptx::warp_max_f32(z[h] + lk);
+            if (lane == 0) S.xmax[hq][q4][h] = x;
+          }
+          group_sync(hq);
+#pragma unroll
+          for (int h = 0; h < kHT; ++h) {
+            const float e = fmaxf(fmaxf(S.xmax[hq][0][h], S.xmax[hq][1][h]), fmaxf(S.xmax[hq][2][h], S.xmax[hq][3][h]));
+            f[h] = 1.f;
+            if (e != -INFINITY && !(e - M[h] <= kCap)) {
+              const float Mn = ceilf(e - kHead);
+              if (M[h] != -INFINITY) {
+                const float d = M[h] - Mn;   // a negative integer
+                f[h] = d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23);
+                lrow[h] *= f[h];
+                any = true;
+              }
+              M[h] = Mn;
+            }
+          }
+        }
+        // The last tile's PV reads the weights and accumulates into O: it is
+        // waited for before either changes (of the piece before, by its epilogue).
+        if (jj > 0) {
+          ok = warp_wait(&S.pv_done, (k - 1) & 1, abort);
+          if (!ok) {
+            *abort = 1;
+            continue;   // the next softmax_all ends every softmax warp
+          }
+          if (any) {
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < 8; ++b) {   // (block, term): this thread's latent dim, this quarter's heads
+              uint32_t ov[kHT];
+              const uint32_t a = T0 + kColO + kHU * b + kHT * hq + lane_off;
+              tmem_ldn(a, ov);
+              ptx::tmem_wait_ld(ov);
+#pragma unroll
+              for (int h = 0; h < kHT; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * f[h]);
+              tmem_stn(a, ov);
+            }
+            ptx::tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < kHT; ++h) {
+          const float p = z[h] == -INFINITY ? 0.f : ex2(z[h] - M[h]);
+          lrow[h] += p;
+          z[h] = p;
+        }
+        // weights as [high | low] terms, keys by heads
+        if constexpr (F::kBf) {
+          const uint32_t pb = ptx::smem_u32(S.pb[0]) + (row >> 3) * kGroupBf<kHU> + (row & 7) * 16;
+#pragma unroll
+          for (int i = 0; i < kHT / 4; ++i) {
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const __nv_bfloat162 hv = __floats2bfloat162_rn(z[4 * i + 2 * c], z[4 * i + 2 * c + 1]);
+              const float2 hf = __bfloat1622float2(hv);
+              const __nv_bfloat162 lv = __floats2bfloat162_rn(z[4 * i + 2 * c] - hf.x, z[4 * i + 2 * c + 1] - hf.y);
+              hi[c] = *reinterpret_cast<const uint32_t*>(&hv);
+              lo[c] = *reinterpret_cast<const uint32_t*>(&lv);
+            }
+            const int hd = kHT * hq + 4 * i;   // first of four heads: 16-B chunk hd / 8
+            st_v2(pb + (hd >> 3) * 128 + (hd & 7) * 2, hi[0], hi[1]);
+            st_v2(pb + (kHU / 8 + (hd >> 3)) * 128 + (hd & 7) * 2, lo[0], lo[1]);
+          }
+        } else {
+          const int hd = kHT * hq;   // 16-B chunk hd / 16
+          const uint32_t off = (row >> 3) * (kHU * 16) + (row & 7) * 16 + (hd >> 4) * 128 + (hd & 15);
+#pragma unroll
+          for (int b = 0; b < F::kSets; ++b) {
+            const uint32_t pb = off + (Sm::kOverlay && b >= 2 ? ptx::smem_u32(S.pe[buf]) + (b - 2) * Sm::kSetBytes
+                                                              : ptx::smem_u32(S.pb[Sm::kOverlay ? b & 1 : b]));
+            uint32_t hi[kHT / 4], lo[kHT / 4];
+#pragma unroll
+            for (int i = 0; i < kHT / 4; ++i) {
+              uint32_t h01, l01, h23, l23;
+              split2_e4m3x2(z[4 * i] * scv[b], z[4 * i + 1] * scv[b], h01, l01);
+              split2_e4m3x2(z[4 * i + 2] * scv[b], z[4 * i + 3] * scv[b], h23, l23);
+              hi[i] = h01 | (h23 << 16);
+              lo[i] = l01 | (l23 << 16);
+            }
+            if constexpr (kHT == 4) {
+              st_b32(pb, hi[0]);
+              st_b32(pb + (kHU / 16) * 128, lo[0]);
+            } else {
+              st_v2(pb, hi[0], hi[1]);
+              st_v2(pb + (kHU / 16) * 128, lo[0], lo[1]);
+            }
+          }
+        }
+        // A masked row may hold anything, and 0 x NaN is NaN in the product:
+        // it is zeroed (QK^T, done with this tile, only ever spoiled that
+        // row's own logits).
+        if (!valid) {
+#pragma unroll
+          for (int b = hq; b < F::kBlocks; b += 4) {
+            const uint32_t a = ptx::smem_u32(S.lat[buf][b]) + (row >> 3) * 1024 + (row & 7) * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) st_v4(a + 16 * c, 0u, 0u, 0u, 0u);
+          }
+        }
+        ptx::fence_proxy_async();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.p_full);
+      }
+      // the next piece's query, before this one's epilogue: its first QK^T is
+      // issued ahead of the PV that the epilogue waits for
+      {
+        Walk peek = w;
+        Seg nx;
+        while (ok && walk_next(P, peek, slot, kHU, nx)) {
+          if (nx.ne > 0) {
+            stage(nx);
+            staged = true;
+            break;
+          }
+        }
+      }
+      // ---- epilogue ----
+      ok = ok && warp_wait(&S.pv_done, (k - 1) & 1, abort);
+      if (!ok) *abort = 1;
+      ok = softmax_all(ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < kHT; ++h) {
+        float v = lrow[h];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) S.xsum[hq][q4][h] = v;
+      }
+      group_sync(hq);
+      float osc[kHT];
+#pragma unroll
+      for (int h = 0; h < kHT; ++h) {
+        const float l = S.xsum[hq][0][h] + S.xsum[hq][1][h] + S.xsum[hq][2][h] + S.xsum[hq][3][h];
+        osc[h] = l > 0.f ? (F::kPlain ? P.latent_scale : 1.f) / l : l == 0.f ? 0.f : l;   // NaN stays
+        if (q4 == 0 && lane == 0) {
+          const float lse = l == 0.f ? -INFINITY : (M[h] + log2f(l)) * kLn2;
+          if (s.whole) P.lse[orow + kHT * hq + h] = lse;
+          else P.ws.part_lse[s.part + kHT * hq + h] = lse;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t hi[kHT], lo[kHT];
+        const uint32_t a = T0 + kColO + 2 * kHU * b + kHT * hq + lane_off;
+        tmem_ldn(a, hi);
+        tmem_ldn(a + kHU, lo);
+        ptx::tmem_wait_ld(hi, lo);
+        const int dim = 128 * b + row;
+#pragma unroll
+        for (int h = 0; h < kHT; ++h) {
+          const float o = (__uint_as_float(hi[h]) + __uint_as_float(lo[h])) * osc[h] * ebi[b];
+          if (s.whole) {
+            const __nv_bfloat16 r = __float2bfloat16_rn(o);
+            P.out[(orow + kHT * hq + h) * SML_LATENT_DIM + dim] = *reinterpret_cast<const uint16_t*>(&r);
+          } else {
+            P.ws.part_out[(s.part + kHT * hq + h) * SML_LATENT_DIM + dim] = o;
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.o_free);
+    }
+    if (!ok) *abort = 1;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && S.abort) raise_fault(P.status, SML_FAULT_TIMEOUT);
+  if (warp == kWarpMma) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(S.tmem_base, 512);
   }
 }
 
 // out = sum_i exp(lse_i - lse) O_i, lse = ln sum_i exp(lse_i) over the pieces
 // of one token that several CTAs hold.  One block per (CTA, head of its unit);
 // only the CTA after the one that begins a split token has something to join.
-__global__ void __launch_bounds__(128) paged_join_kernel(int H, PagedWs ws, uint16_t* __restrict__ out,
+__global__ void __launch_bounds__(128) paged_join_kernel(int H, int heads, PagedWs ws, uint16_t* __restrict__ out,
                                                          float* __restrict__ lse) {
   const int c = blockIdx.x, hl = blockIdx.y, g = c / ws.cpg;
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int4 rec = __ldcg(ws.join + c);
   if (rec.x < 0) return;
-  auto row = [&](int i) { return (size_t)((g * ws.cpg + i) * 2 + (i == rec.y)) * kHU + hl; };
+  auto row = [&](int i) { return (size_t)((g * ws.cpg + i) * 2 + (i == rec.y)) * heads + hl; };
   float m = -INFINITY;
   for (int i = rec.y; i <= rec.z; ++i) m = fmaxf(m, __ldcg(ws.part_lse + row(i)));
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -331,20 +990,36 @@ __global__ void __launch_bounds__(128) paged_join_kernel(int H, PagedWs ws, uint
     o.w = fmaf(w, v.w, o.w);
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;
-  const size_t orow = (size_t)rec.x * H + g * kHU + hl;
+  const size_t orow = (size_t)rec.x * H + g * heads + hl;
   const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   reinterpret_cast<uint2*>(out + orow * SML_LATENT_DIM)[threadIdx.x] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   if (threadIdx.x == 0) lse[orow] = den > 0.f ? m + logf(den) : -INFINITY;
 }
 
+template <int kFmt, int kHU>
+cudaError_t launch_unit(const CUtensorMap& rows, const CUtensorMap& scales, const Params& P, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem<kFmt, kHU>) + 1024;
+  auto kernel = paged_mla_kernel<kFmt, kHU>;
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(P.ws.hg * P.ws.cpg), dim3(kThreads), smem, stream, 0, rows, scales, P);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_join_kernel, dim3(P.ws.hg * P.ws.cpg, kHU), dim3(128), 0, stream, 0, P.H, kHU, P.ws, P.out, P.lse);
+}
+
+template <int kFmt>
+cudaError_t launch_format(const CUtensorMap& rows, const CUtensorMap& scales, const Params& P, cudaStream_t stream) {
+  return P.H == 16 ? launch_unit<kFmt, 16>(rows, scales, P, stream) : launch_unit<kFmt, 32>(rows, scales, P, stream);
+}
+
 }  // namespace
 
-int paged_heads(const sml_problem&) { return kHU; }
+int paged_heads(const sml_problem& p) { return p.num_heads == 16 ? 16 : 32; }
 
 PagedWs paged_plan(const sml_problem& p) {
   PagedWs w = {};
-  w.hg = p.num_heads / kHU;
+  w.hg = p.num_heads / paged_heads(p);
   w.cpg = device_sm_count() / w.hg > 0 ? device_sm_count() / w.hg : 1;
   return w;
 }
@@ -367,20 +1042,33 @@ cudaError_t launch_paged_mla(const sml_problem& p, const uint16_t* q, const sml_
   P.vis_len = p.vis_len;
   P.ssmax_len = p.ssmax_len;
   P.q = q;
-  P.latent = static_cast<const uint8_t*>(latent.base);
   P.latent_pages = latent.num_pages;
-  P.format = latent.format;
-  P.latent_scale = latent.scale;
+  P.latent_scale = latent.format == SML_LATENT_E4M3 ? latent.scale : 1.f;
   P.sel = sel;
   P.out = out;
   P.lse = lse;
   P.ws = ws;
   P.status = status;
-  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(paged_mla_kernel), sizeof(Smem));
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_mla_kernel, dim3(ws.hg * ws.cpg), dim3(kThreads), sizeof(Smem), stream, 0, P);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(paged_join_kernel, dim3(ws.hg * ws.cpg, kHU), dim3(128), 0, stream, 0, p.num_heads, ws, out, lse);
+  // The pool as rows of bytes: one box is a 128-B column of a page's 64 rows
+  // (a row's last box may reach past its end: zeros), or its 64 x 4 block scales.
+  const auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t row = latent.format == SML_LATENT_BF16   ? SML_LATENT_BF16_ROW_BYTES
+                         : latent.format == SML_LATENT_E4M3 ? SML_LATENT_E4M3_ROW_BYTES
+                                                            : SML_LATENT_ROW_BYTES;
+  const cuuint64_t dims[2] = {row, (cuuint64_t)latent.num_pages * SML_PAGE_TOKENS}, strides[1] = {row};
+  const cuuint32_t box[2] = {128, SML_PAGE_TOKENS}, sbox[2] = {16, SML_PAGE_TOKENS}, one[2] = {1, 1};
+  CUtensorMap rows, scales;
+  if (enc(&rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(latent.base), dims, strides, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+      enc(&scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(latent.base), dims, strides, sbox, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  if (latent.format == SML_LATENT_BF16) return launch_format<kFmtBf16>(rows, scales, P, stream);
+  if (latent.format == SML_LATENT_E4M3) return launch_format<kFmtPlain>(rows, scales, P, stream);
+  return launch_format<kFmtDsMla>(rows, scales, P, stream);
 }
 
 }  // namespace sml

@@ -2,6 +2,7 @@
 #pragma once
 #include <utility>
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -179,6 +180,7 @@ __device__ __forceinline__ int ssmax_len_of(const int32_t* __restrict__ ssl, int
 // Host-side per-device caches for the launchers (thread-safe): the SM count,
 // and the dynamic shared-memory attribute, set once per kernel and device.
 int device_sm_count();
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // null if the driver has none
 cudaError_t set_max_smem(const void* func, size_t bytes);
 
 // Launch with programmatic stream serialization: the kernel may be scheduled
