@@ -21,11 +21,12 @@ namespace sml {
 namespace {
 
 constexpr int kKT = 128;                 // keys per tile: two pages
+constexpr int kParts = 4;                // a tile's latent dims arrive and are freed in quarters of 128
 constexpr int kLatBlock = kKT * 128;     // one 128-B wide block of a tile
 constexpr int kSoftmaxWarps = 16;        // warps 0-15
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kWarpMma = 16, kWarpLoad = 17;
-constexpr int kThreads = 576;
+constexpr int kWarpQk = 16, kWarpPv = 17, kWarpLoad = 18;
+constexpr int kThreads = 608;
 constexpr uint32_t kColO = 256;          // TMEM: logits from column 0, O from here
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -206,8 +207,8 @@ struct __align__(1024) Smem {
   float xsum[4][4][kHU / 4];
   float qs[kHU];                                  // power-of-two query scale per head
   int4 rows[4];                                   // [tile % 4] valid rows {lo, hi} of each page of the tile
-  uint64_t full[F::kBufs], lat_free[F::kBufs];
-  uint64_t q_ready, s_full, s_free, p_full, pv_done, o_free, drain;
+  uint64_t full[F::kBufs][kParts], lat_free[F::kBufs][kParts];   // per quarter of the latent dims
+  uint64_t q_ready, s_full, s_free, p_full, pv_done, o_free, drain[2];
   uint32_t tmem_base;
   int abort;
   PlanSmem plan;
@@ -429,9 +430,9 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
   const int g = (int)blockIdx.x % P.ws.hg, gi = (int)blockIdx.x / P.ws.hg;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kBufs; ++i) {
-      ptx::mbar_init(&S.full[i], 1);
-      ptx::mbar_init(&S.lat_free[i], 1);
+    for (int i = 0; i < kBufs * kParts; ++i) {
+      ptx::mbar_init(&S.full[0][0] + i, 1);
+      ptx::mbar_init(&S.lat_free[0][0] + i, 1);
     }
     ptx::mbar_init(&S.q_ready, 16 * kHU / 32);
     ptx::mbar_init(&S.s_full, 1);
@@ -439,11 +440,12 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     ptx::mbar_init(&S.p_full, kSoftmaxWarps);
     ptx::mbar_init(&S.pv_done, 1);
     ptx::mbar_init(&S.o_free, kSoftmaxWarps);
-    ptx::mbar_init(&S.drain, 1);
+    ptx::mbar_init(&S.drain[0], 1);
+    ptx::mbar_init(&S.drain[1], 1);
     S.abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == kWarpMma) {
+  if (warp == kWarpQk) {
     ptx::tmem_alloc(&S.tmem_base, 512);
     ptx::tmem_relinquish();
   }
@@ -477,11 +479,12 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     // ================= producer: page ids, then TMA =================
     Walk w = begin;
     Seg s;
-    int k = 0;   // tiles so far
+    int k = 0, begun = 0;   // tiles so far, and parts of the next one
     bool ok = true;
     const bool rope = P.rope_dim != 0;
-    constexpr uint32_t kPageBytes = F::kBlocks * SML_PAGE_TOKENS * 128 + (F::kDs ? SML_PAGE_TOKENS * 16 : 0);
-    const uint32_t page_bytes = kPageBytes + (rope ? SML_PAGE_TOKENS * 128 : 0);
+    constexpr int kPartBlocks = F::kBlocks / kParts;
+    constexpr uint32_t kPartBytes = kPartBlocks * SML_PAGE_TOKENS * 128;   // of one page
+    const uint32_t last_bytes = kPartBytes + (F::kDs ? SML_PAGE_TOKENS * 16 : 0) + (rope ? SML_PAGE_TOKENS * 128 : 0);
     while (ok && walk_next(P, w, slot, kHU, s)) {
       if (lane == 0 && g == 0) {
         if (!s.tk.ok) raise_fault(P.status, SML_FAULT_LENGTHS);
@@ -493,86 +496,131 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         if (two == 0) ph = page_at(P, s.tk, s.t, 2 * (s.j0 + jj) + lane, lane < 2 * (s.ne - jj), &lg);
         const int p0 = __shfl_sync(0xffffffffu, ph, two), p1 = __shfl_sync(0xffffffffu, ph, two + 1);
         const int l0 = __shfl_sync(0xffffffffu, lg, two), l1 = __shfl_sync(0xffffffffu, lg, two + 1);
-        if (k >= kBufs) ok = warp_wait(&S.lat_free[buf], ((k / kBufs) - 1) & 1, abort);
-        if (!ok) break;
-        if (lane == 0) {
-          int4 r;   // valid rows of each page: none of one that is not loaded
-          r.x = max(0, s.tk.lo - l0 * SML_PAGE_TOKENS);
-          r.y = p0 >= 0 ? min(SML_PAGE_TOKENS, s.tk.n - l0 * SML_PAGE_TOKENS) : 0;
-          r.z = max(0, s.tk.lo - l1 * SML_PAGE_TOKENS);
-          r.w = p1 >= 0 ? min(SML_PAGE_TOKENS, s.tk.n - l1 * SML_PAGE_TOKENS) : 0;
-          S.rows[k & 3] = r;   // last read by the softmax of tile k - 4
-          ptx::mbar_arrive_expect_tx(&S.full[buf], ((p0 >= 0) + (p1 >= 0)) * page_bytes);
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const int pg = half ? p1 : p0;
-            if (pg < 0) continue;
-            const int y = pg * SML_PAGE_TOKENS, off = half * SML_PAGE_TOKENS * 128;
-            // what the logits wait for first: scales and RoPE are small
-            if (F::kDs) ptx::tma_load_2d(&S.sc[F::kDs ? buf : 0][half * SML_PAGE_TOKENS][0], &scale_map, &S.full[buf], SML_LATENT_DIM, y);
+        const uint32_t pages = (p0 >= 0) + (p1 >= 0);
+        // The last part brings the scales and the RoPE keys: with 32 heads the
+        // RoPE keys' place holds the weights of the last two parts until then.
+        for (int part = 0; part < kParts; ++part) {
+          begun = part;
+          if (k >= kBufs) ok = warp_wait(&S.lat_free[buf][part], ((k / kBufs) - 1) & 1, abort);
+          if (!ok) break;
+          if (lane == 0) {
+            const bool last = part == kParts - 1;
+            if (last) {
+              int4 r;   // valid rows of each page: none of one that is not loaded
+              r.x = max(0, s.tk.lo - l0 * SML_PAGE_TOKENS);
+              r.y = p0 >= 0 ? min(SML_PAGE_TOKENS, s.tk.n - l0 * SML_PAGE_TOKENS) : 0;
+              r.z = max(0, s.tk.lo - l1 * SML_PAGE_TOKENS);
+              r.w = p1 >= 0 ? min(SML_PAGE_TOKENS, s.tk.n - l1 * SML_PAGE_TOKENS) : 0;
+              S.rows[k & 3] = r;   // last read by the softmax of tile k - 4
+            }
+            uint64_t* bar = &S.full[buf][part];
+            ptx::mbar_arrive_expect_tx(bar, pages * (last ? last_bytes : kPartBytes));
 #pragma unroll
-            for (int b = 0; b < F::kBlocks; ++b)
-              ptx::tma_load_2d(S.lat[buf][b] + off, &row_map, &S.full[buf], 128 * b, y);
-            if (rope) ptx::tma_load_2d(S.pe[buf] + off, &row_map, &S.full[buf], F::kPeX, y);
+            for (int half = 0; half < 2; ++half) {
+              const int pg = half ? p1 : p0, y = pg * SML_PAGE_TOKENS, off = half * SML_PAGE_TOKENS * 128;
+              if (pg < 0) continue;
+#pragma unroll
+              for (int b = 0; b < kPartBlocks; ++b)
+                ptx::tma_load_2d(S.lat[buf][part * kPartBlocks + b] + off, &row_map, bar, 128 * (part * kPartBlocks + b), y);
+              if (last && F::kDs)
+                ptx::tma_load_2d(&S.sc[F::kDs ? buf : 0][half * SML_PAGE_TOKENS][0], &scale_map, bar, SML_LATENT_DIM, y);
+              if (last && rope) ptx::tma_load_2d(S.pe[buf] + off, &row_map, bar, F::kPeX, y);
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
+        begun = 0;
       }
     }
     if (!ok) *abort = 1;
     // nothing of this CTA's in flight when its shared memory goes away
-    for (int i = max(0, k - kBufs); i < k; ++i) ptx::mbar_wait(&S.full[i % kBufs], (i / kBufs) & 1, nullptr, 100000u);
+    for (int part = 0; part < kParts; ++part) {
+      const int n = k + (part < begun);   // loads of this part so far
+      for (int i = max(0, n - kBufs); i < n; ++i)
+        ptx::mbar_wait(&S.full[i % kBufs][part], (i / kBufs) & 1, nullptr, 100000u);
+    }
     __syncwarp();
-  } else if (warp == kWarpMma) {
-    // ================= MMA issuer =================
-    const uint32_t id_qk = F::kBf ? ptx::idesc_f16(kHU, 1, 0, 0) : ptx::idesc_f16(kHU, 0, 0, 0);
-    const uint32_t id_pe = ptx::idesc_f16(kHU, 1, 0, 0);
-    const uint32_t id_pv = F::kBf ? ptx::idesc_f16(2 * kHU, 1, 1, 1) : ptx::idesc_f16(2 * kHU, 0, 1, 1);
+  } else if (warp == kWarpQk) {
+    // ================= QK^T issuer =================
+    constexpr uint32_t id_qk = F::kBf ? ptx::idesc_f16(kHU, 1, 0, 0) : ptx::idesc_f16(kHU, 0, 0, 0);
+    constexpr uint32_t id_pe = ptx::idesc_f16(kHU, 1, 0, 0);
     const uint32_t q0 = ptx::smem_u32(S.q8), qp = ptx::smem_u32(S.qpe);
-    auto issue_qk = [&](int buf) {
-      const uint32_t pe0 = ptx::smem_u32(S.pe[buf]);
+    // One part of a tile's QK^T: 128 latent dims, and with the last the RoPE dims.
+    auto issue_qk = [&](int buf, int part) {
       if constexpr (F::kBf) {
         // S^T = C . Q^T + K_pe . Q_pe^T, 16 dims per step
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
+        for (int bb = 0; bb < 2; ++bb)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_f16_ss(T0, ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
-                            ptx::sdesc_sw128(q0 + b * (kHU * 128) + 32 * kk), id_qk, (b | kk) != 0);
-        if (P.rope_dim) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_f16_ss(T0, ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk), id_qk, 1);
-        }
+          for (int kk = 0; kk < 4; ++kk) {
+            const int b = 2 * part + bb;
+            ptx::mma_bf(T0, ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
+                        ptx::sdesc_sw128(q0 + b * (kHU * 128) + 32 * kk), id_qk, (part | bb | kk) != 0);
+          }
       } else {
         // S_b^T = C_b . (Qhi_b + Qlo_b)^T, 32 dims per step (plain E4M3: one sum over the blocks)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int term = 0; term < 2; ++term)
+            ptx::mma_f8(T0 + (F::kDs ? kHU * part : 0), ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][part]) + 32 * kk),
+                        ptx::sdesc_sw128(q0 + (2 * part + term) * (kHU * 128) + 32 * kk), id_qk,
+                        F::kDs ? (kk | term) != 0 : (part | kk | term) != 0);
+      }
+      if (part < kParts - 1) return;
+      const uint32_t pe0 = ptx::smem_u32(S.pe[buf]);
+      if (P.rope_dim) {
+        if constexpr (F::kPlain) {
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int term = 0; term < 2; ++term)
-              ptx::mma_f8f6f4_ss(T0 + (F::kDs ? kHU * b : 0), ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
-                                 ptx::sdesc_sw128(q0 + (2 * b + term) * (kHU * 128) + 32 * kk), id_qk,
-                                 F::kDs ? (kk | term) != 0 : (kk | b | term) != 0);
-        if (P.rope_dim) {
-          if (F::kDs) {
+              ptx::mma_f8(T0, ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + term * (kHU * 128) + 32 * kk), id_qk, true);
+        } else {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::mma_f16_ss(T0 + 4 * kHU, ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk), id_pe, kk > 0);
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-              for (int term = 0; term < 2; ++term)
-                ptx::mma_f8f6f4_ss(T0, ptx::sdesc_sw128(pe0 + 32 * kk),
-                                   ptx::sdesc_sw128(qp + term * (kHU * 128) + 32 * kk), id_qk, 1);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_bf(T0 + (F::kDs ? 4 * kHU : 0), ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk), id_pe,
+                        F::kBf || kk > 0);
         }
       }
       ptx::mma_commit(&S.s_full);
     };
-    // O_b^T (+)= C_b^T . [Bhi_b; Blo_b]^T.  A: the tile read MN-major (dims
+    // One elected lane issues, from code with the buffer and part known at
+    // compile time, so that the descriptors are constants off a uniform base.
+    Cur c;
+    c.w = begin;
+    c.seg = c.k = 0;
+    cur_seek(c, P);
+    bool ok = true;
+    for (; c.valid; cur_next(c, P)) {
+      const int buf = c.k % kBufs;
+      if (c.jj == 0) ok = warp_wait(&S.q_ready, c.seg & 1, abort);                    // the piece's query is staged
+      if (ok && c.k > 0) ok = warp_wait(&S.s_free, (c.k - 1) & 1, abort);             // the last tile's S has been read
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        ok = ok && warp_wait(&S.full[buf][part], (c.k / kBufs) & 1, abort);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          if (buf == 0) issue_qk(0, part);
+          else issue_qk(kBufs - 1, part);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    if (!ok) *abort = 1;
+    // every MMA issued has finished before TMEM is released
+    if (ptx::elect_one()) ptx::mma_commit(&S.drain[0]);
+    __syncwarp();
+    ptx::mbar_wait(&S.drain[0], 0, nullptr, 100000u);
+    __syncwarp();
+  } else if (warp == kWarpPv) {
+    // ================= PV issuer =================
+    constexpr uint32_t id_pv = F::kBf ? ptx::idesc_f16(2 * kHU, 1, 1, 1) : ptx::idesc_f16(2 * kHU, 0, 1, 1);
+    // O_b^T (+)= C_b^T . [Bhi_b; Blo_b]^T for the four 128-dim output blocks,
+    // each freeing its part of the tile.  A: the tile read MN-major (dims
     // contiguous; 8-key swizzle atoms 1,024 B apart; of a bf16 tile the two
     // 64-dim atoms of an output block 16 KB apart).  B: 8-key x 16-B core
     // matrices, along the heads 128 B apart.
@@ -580,76 +628,45 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     constexpr uint32_t kGroup = 2 * kHU * (F::kBf ? 2 : 1) * 8;   // bytes of an 8-key group of a weight set
     auto issue_pv = [&](int buf, bool first) {
 #pragma unroll
-      for (int st = 0; st < kKT / kKeysPerStep; ++st)
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t set = F::kSets == 1 ? ptx::smem_u32(S.pb[0])
+                             : Sm::kOverlay && b >= 2 ? ptx::smem_u32(S.pe[buf]) + (b - 2) * Sm::kSetBytes
+                                                      : ptx::smem_u32(S.pb[Sm::kOverlay ? b & 1 : b]);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t set = F::kSets == 1 ? ptx::smem_u32(S.pb[0])
-                               : Sm::kOverlay && b >= 2 ? ptx::smem_u32(S.pe[buf]) + (b - 2) * Sm::kSetBytes
-                                                        : ptx::smem_u32(S.pb[Sm::kOverlay ? b & 1 : b]);
+        for (int st = 0; st < kKT / kKeysPerStep; ++st) {
           const uint64_t bd = ptx::sdesc(set + st * (kKeysPerStep / 8) * kGroup, kGroup, 128, 0);
           const uint32_t d = T0 + kColO + 2 * kHU * b;
           if constexpr (F::kBf)
-            ptx::mma_f16_ss(d, ptx::sdesc(ptx::smem_u32(S.lat[buf][2 * b]) + 2048 * st, 16384, 1024, 2), bd, id_pv, !first || st > 0);
+            ptx::mma_bf(d, ptx::sdesc(ptx::smem_u32(S.lat[buf][2 * b]) + 2048 * st, 16384, 1024, 2), bd, id_pv, st > 0 || !first);
           else
-            ptx::mma_f8f6f4_ss(d, ptx::sdesc(ptx::smem_u32(S.lat[buf][b]) + 4096 * st, 16384, 1024, 2), bd, id_pv, !first || st > 0);
+            ptx::mma_f8(d, ptx::sdesc(ptx::smem_u32(S.lat[buf][b]) + 4096 * st, 16384, 1024, 2), bd, id_pv, st > 0 || !first);
         }
+        if (b < 3) ptx::mma_commit(&S.lat_free[buf][b]);
+      }
       ptx::mma_commit(&S.pv_done);
-      ptx::mma_commit(&S.lat_free[buf]);
+      ptx::mma_commit(&S.lat_free[buf][3]);
     };
-    // The next QK^T and the next PV: whichever is ready goes first, QK^T at
-    // most one tile ahead.  A tile's QK^T needs its rows, the last S read and,
-    // for the first tile of a piece, the staged query; its PV needs its weights
-    // and, for the first tile of a later piece, the last O read.
-    Cur cq;
-    cq.w = begin;
-    cq.seg = cq.k = 0;
-    cur_seek(cq, P);
-    Cur cv = cq;
+    Cur c;
+    c.w = begin;
+    c.seg = c.k = 0;
+    cur_seek(c, P);
     bool ok = true;
-    uint32_t idle = 0;
-    while (ok && cv.valid) {
-      int act = 0;   // 1: PV of cv, 2: QK^T of cq, -1: gave up
-      if (lane == 0) {
-        const bool pv_first = cv.jj == 0 && cv.seg > 0;
-        if (cv.k < cq.k && ptx::mbar_test_wait(&S.p_full, cv.k & 1) &&
-            (!pv_first || ptx::mbar_test_wait(&S.o_free, (cv.seg - 1) & 1))) {
-          act = 1;
-        } else if (cq.valid && cq.k <= cv.k + 1 && (cq.jj > 0 || ptx::mbar_test_wait(&S.q_ready, cq.seg & 1)) &&
-                   ptx::mbar_test_wait(&S.full[cq.k % kBufs], (cq.k / kBufs) & 1) &&
-                   (cq.k == 0 || ptx::mbar_test_wait(&S.s_free, (cq.k - 1) & 1))) {
-          act = 2;
-        } else if (*abort || ++idle > (1u << 22)) {
-          act = -1;
-        } else {
-          // sleep on the barrier the next step most likely waits for
-          if (cv.k < cq.k) ptx::mbar_try_wait_ns(&S.p_full, cv.k & 1, 200);
-          else if (cq.valid) ptx::mbar_try_wait_ns(&S.full[cq.k % kBufs], (cq.k / kBufs) & 1, 200);
-        }
-        if (act == 1) {
-          ptx::tc_fence_after();
-          issue_pv(cv.k % kBufs, cv.jj == 0);
-        } else if (act == 2) {
-          ptx::tc_fence_after();
-          issue_qk(cq.k % kBufs);
-        }
+    for (; c.valid; cur_next(c, P)) {
+      const int buf = c.k % kBufs;
+      if (c.jj == 0 && c.seg > 0) ok = warp_wait(&S.o_free, (c.seg - 1) & 1, abort);  // the last piece's O has been read
+      ok = ok && warp_wait(&S.p_full, c.k & 1, abort);                                // weights written, masked rows zeroed
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        if (buf == 0) issue_pv(0, c.jj == 0);
+        else issue_pv(kBufs - 1, c.jj == 0);
       }
-      act = __shfl_sync(0xffffffffu, act, 0);
-      if (act == 1) {
-        cur_next(cv, P);
-        idle = 0;
-      } else if (act == 2) {
-        cur_next(cq, P);
-        idle = 0;
-      } else if (act < 0) {
-        ok = false;
-      }
+      __syncwarp();
     }
-    if (lane == 0) {
-      if (!ok) *abort = 1;
-      // every MMA this thread issued has finished before TMEM is released
-      ptx::mma_commit(&S.drain);
-      ptx::mbar_wait(&S.drain, 0, nullptr, 100000u);
-    }
+    if (!ok) *abort = 1;
+    if (ptx::elect_one()) ptx::mma_commit(&S.drain[1]);
+    __syncwarp();
+    ptx::mbar_wait(&S.drain[1], 0, nullptr, 100000u);
     __syncwarp();
   } else if (warp < kSoftmaxWarps) {
     // ================= softmax =================
@@ -701,7 +718,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       float ebf[4] = {1.f, 1.f, 1.f, 1.f}, ebi[4] = {1.f, 1.f, 1.f, 1.f};
       for (int jj = 0; jj < s.ne; ++jj, ++k) {
         const int buf = k % kBufs;
-        ok = ok && warp_wait(&S.full[buf], (k / kBufs) & 1, abort) && warp_wait(&S.s_full, k & 1, abort);
+        ok = ok && warp_wait(&S.full[buf][kParts - 1], (k / kBufs) & 1, abort) && warp_wait(&S.s_full, k & 1, abort);
         if (!ok) *abort = 1;
         ok = softmax_all(ok);
         if (!ok) break;
@@ -959,7 +976,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
   ptx::tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && S.abort) raise_fault(P.status, SML_FAULT_TIMEOUT);
-  if (warp == kWarpMma) {
+  if (warp == kWarpQk) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(S.tmem_base, 512);
   }
