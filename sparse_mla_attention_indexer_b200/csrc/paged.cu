@@ -27,6 +27,7 @@ constexpr int kSoftmaxWarps = 16;        // warps 0-15
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kWarpQk = 16, kWarpPv = 17, kWarpLoad = 18;
 constexpr int kThreads = 608;
+constexpr int kAhead = 2;                // tiles between an L2 prefetch and the tile being loaded
 constexpr uint32_t kColO = 256;          // TMEM: logits from column 0, O from here
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -46,6 +47,7 @@ struct Params {
   const int32_t* vis_len;
   const int32_t* ssmax_len;
   const uint16_t* q;
+  const uint8_t* latent;
   int64_t latent_pages;
   float latent_scale;
   PagedSel sel;
@@ -183,8 +185,16 @@ template <int kFmt>
 struct Fmt {
   static constexpr bool kDs = kFmt == kFmtDsMla, kPlain = kFmt == kFmtPlain, kBf = kFmt == kFmtBf16;
   static constexpr int kBufs = kBf ? 1 : 2;        // tile buffers (a bf16 tile is 144 KB)
+  static constexpr uint32_t kPageBytes = kBf ? SML_LATENT_BF16_PAGE_BYTES : kPlain ? SML_LATENT_E4M3_PAGE_BYTES : SML_LATENT_PAGE_BYTES;
   static constexpr int kBlocks = kBf ? 8 : 4;      // 128-B wide blocks of a tile's latents
   static constexpr int kSets = kDs ? 4 : 1;        // weight sets: one per block scale
+  // Logit accumulators: one per block scale, and RoPE's.  Both query terms'
+  // columns stand side by side (one MMA of twice the width costs about as much
+  // as one: 46 cycles at N = 32, 55 at 64), except those of the last block
+  // where 32 heads would leave no room for them beside O: they are summed.
+  static constexpr bool split_terms(int heads, int b) { return !kBf && !(kDs && heads == 32 && b == 3); }
+  static constexpr uint32_t col_block(int heads, int b) { return kDs ? 2 * heads * b : 0; }
+  static constexpr uint32_t col_rope(int heads) { return heads == 32 ? 224 : 128; }
   static constexpr int kPeX = kBf ? 2 * SML_LATENT_DIM : kPlain ? SML_LATENT_DIM : SML_LATENT_DIM + 16;
 };
 
@@ -293,17 +303,21 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float& x0, float& x1) {
   x1 -= r.y;
   return c;
 }
-// Two weights (each at most 448) as two E4M3 terms, hi + lo: eight significant
-// bits, as many as a bf16 has.  The residual is taken in half precision, where
-// both the rounded weight (2^-11) and the difference fit: three conversions
-// and one subtraction for two weights.
-__device__ __forceinline__ void split2_e4m3x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __half2 x = __floats2half2_rn(x0, x1);
-  const __half2_raw xr = *reinterpret_cast<const __half2_raw*>(&x);
-  hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(xr, __NV_SATFINITE, __NV_E4M3) & 0xffffu;
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
-  const __half2 r = __hsub2(x, *reinterpret_cast<const __half2*>(&b));
-  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
+// Two weights (at most 448) in half precision as two E4M3 terms, hi + lo: eight
+// significant bits, as many as a bf16 has.  hi is x to 4 significant bits by
+// Veltkamp's splitting (T. J. Dekker, "A floating-point technique for extending
+// the available precision", 1971): c = 129 x rounded, hi = c + (x - c); 129 *
+// 448 fits half precision (the _rn forms: a fused multiply-add would undo the
+// rounding that the splitting rests on).  x - hi is exact.  Below E4M3's smallest normal
+// value 2^-6 each term is off by at most half a subnormal step, 2^-10.
+__device__ __forceinline__ uint32_t half2_to_e4m3x2(__half2 x) {
+  return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
+}
+__device__ __forceinline__ void split2_e4m3x2(__half2 x, uint32_t& hi, uint32_t& lo) {
+  const __half2 c = __hmul2_rn(x, __float2half2_rn(129.f));
+  const __half2 h = __hadd2_rn(c, __hsub2_rn(x, c));
+  hi = half2_to_e4m3x2(h);
+  lo = half2_to_e4m3x2(__hsub2_rn(x, h));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -343,9 +357,18 @@ __device__ __forceinline__ bool group_any(int hq, bool v) {
 }
 __device__ __forceinline__ void group_sync(int hq) { asm volatile("bar.sync %0, 128;" ::"r"(1 + hq) : "memory"); }
 
+// Column (and query row) of head h's term among 2 heads columns: each head
+// quarter's high terms, then its low terms, so that one thread's are adjacent.
+template <int kHU>
+__device__ __forceinline__ int split_col(int h, int term) {
+  constexpr int kHT = kHU / 4;
+  return (h / kHT) * (2 * kHT) + term * kHT + h % kHT;
+}
+
+__device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[16]) { ptx::tmem_ld16(a, r); }
+__device__ __forceinline__ void tmem_stn(uint32_t a, const uint32_t (&r)[16]) { ptx::tmem_st16(a, r); }
 __device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[4]) { ptx::tmem_ld4(a, r); }
 __device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[8]) { ptx::tmem_ld8(a, r); }
-__device__ __forceinline__ void tmem_stn(uint32_t a, const uint32_t (&r)[4]) { ptx::tmem_st4(a, r); }
 __device__ __forceinline__ void tmem_stn(uint32_t a, const uint32_t (&r)[8]) { ptx::tmem_st8(a, r); }
 
 // Stage the query of (token t, head group g); thread = head x 32-dim part of
@@ -401,15 +424,16 @@ __device__ __forceinline__ void stage_query(const Params& P, Smem<kFmt, kHU>& S,
     split4(v[2 * c + 1].x, v[2 * c + 1].y, hw[2], lw[2]);
     split4(v[2 * c + 1].z, v[2 * c + 1].w, hw[3], lw[3]);
     const int chunk = 2 * (p & 3) + c;
-    st_v4(sw128(qb, h, chunk), hw[0], hw[1], hw[2], hw[3]);
-    st_v4(sw128(qb, h + kHU, chunk), lw[0], lw[1], lw[2], lw[3]);
+    const bool split = F::split_terms(kHU, p >> 2);
+    st_v4(sw128(qb, split ? split_col<kHU>(h, 0) : h, chunk), hw[0], hw[1], hw[2], hw[3]);
+    st_v4(sw128(qb, split ? split_col<kHU>(h, 1) : h + kHU, chunk), lw[0], lw[1], lw[2], lw[3]);
   }
   if (P.rope_dim) {
     if (F::kPlain) {
       uint32_t hi, lo;
       split4(pv.x, pv.y, hi, lo);
-      st_b32(sw128(qp, h, p >> 2) + 4 * (p & 3), hi);
-      st_b32(sw128(qp, h + kHU, p >> 2) + 4 * (p & 3), lo);
+      st_b32(sw128(qp, split_col<kHU>(h, 0), p >> 2) + 4 * (p & 3), hi);
+      st_b32(sw128(qp, split_col<kHU>(h, 1), p >> 2) + 4 * (p & 3), lo);
     } else {
       st_v2(sw128(qp, h, p >> 1) + 8 * (p & 1), pv.x, pv.y);
     }
@@ -464,13 +488,11 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
   const Range R = plan_range<kThreads>(P, gi, S.plan);
   const int slot = (g * P.ws.cpg + gi) * 2;
   if (threadIdx.x == 0) {
-    // the token to join at this CTA: the one it continues, if the CTA before began it
+    // the token that this CTA continues, and the CTAs that hold it
     int4 rec = make_int4(-1, 0, 0, 0);
-    if (gi < R.used && R.ub > R.tok0) {
-      const int i0 = cta_of(R.total, R.used, R.tok0);
-      if (i0 == gi - 1)
-        rec = make_int4(R.t0, i0, cta_of(R.total, R.used, R.tok0 + tiles_of(token_at(P, R.t0)) - 1), 0);
-    }
+    if (gi < R.used && R.ub > R.tok0)
+      rec = make_int4(R.t0, cta_of(R.total, R.used, R.tok0),
+                      cta_of(R.total, R.used, R.tok0 + tiles_of(token_at(P, R.t0)) - 1), gi);
     P.ws.join[g * P.ws.cpg + gi] = rec;
   }
   const Walk begin = {R.ub, R.ue, R.t0, (int)(R.ub - R.tok0)};
@@ -490,10 +512,26 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         if (!s.tk.ok) raise_fault(P.status, SML_FAULT_LENGTHS);
         if (s.tk.len_bad) raise_fault(P.status, SML_FAULT_TOPK_LEN);
       }
-      int ph = -1, lg = 0;   // of page 2 (j0 + 16 i) + lane
+      int ph = -1, lg = 0, phn = -1, lgn = 0;   // of page 2 (j0 + 16 i) + lane, and 32 pages on
       for (int jj = 0; jj < s.ne; ++jj, ++k) {
         const int buf = k % kBufs, two = 2 * (jj & 15);
-        if (two == 0) ph = page_at(P, s.tk, s.t, 2 * (s.j0 + jj) + lane, lane < 2 * (s.ne - jj), &lg);
+        if (two == 0) {
+          if (jj == 0) {
+            ph = page_at(P, s.tk, s.t, 2 * s.j0 + lane, lane < 2 * s.ne, &lg);
+          } else {
+            ph = phn;
+            lg = lgn;
+          }
+          phn = page_at(P, s.tk, s.t, 2 * (s.j0 + jj) + 32 + lane, lane + 32 < 2 * (s.ne - jj), &lgn);
+        }
+        // The tile after next goes to L2 now, so that its loads, issued when a
+        // buffer is free, find it there.  One head group asks for all.
+        if (g == 0 && jj + kAhead < s.ne) {
+          const int i = two + 2 * kAhead;
+          const int a0 = __shfl_sync(0xffffffffu, i < 32 ? ph : phn, i & 31), a1 = __shfl_sync(0xffffffffu, i < 32 ? ph : phn, (i + 1) & 31);
+          const int pg = lane == 0 ? a0 : a1;
+          if (lane < 2 && pg >= 0) ptx::bulk_prefetch_l2(P.latent + (size_t)pg * F::kPageBytes, F::kPageBytes);
+        }
         const int p0 = __shfl_sync(0xffffffffu, ph, two), p1 = __shfl_sync(0xffffffffu, ph, two + 1);
         const int l0 = __shfl_sync(0xffffffffu, lg, two), l1 = __shfl_sync(0xffffffffu, lg, two + 1);
         const uint32_t pages = (p0 >= 0) + (p1 >= 0);
@@ -543,7 +581,8 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     __syncwarp();
   } else if (warp == kWarpQk) {
     // ================= QK^T issuer =================
-    constexpr uint32_t id_qk = F::kBf ? ptx::idesc_f16(kHU, 1, 0, 0) : ptx::idesc_f16(kHU, 0, 0, 0);
+    constexpr uint32_t id_q1 = F::kBf ? ptx::idesc_f16(kHU, 1, 0, 0) : ptx::idesc_f16(kHU, 0, 0, 0);
+    constexpr uint32_t id_q2 = ptx::idesc_f16(2 * kHU, 0, 0, 0);   // both terms
     constexpr uint32_t id_pe = ptx::idesc_f16(kHU, 1, 0, 0);
     const uint32_t q0 = ptx::smem_u32(S.q8), qp = ptx::smem_u32(S.qpe);
     // One part of a tile's QK^T: 128 latent dims, and with the last the RoPE dims.
@@ -556,17 +595,18 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           for (int kk = 0; kk < 4; ++kk) {
             const int b = 2 * part + bb;
             ptx::mma_bf(T0, ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
-                        ptx::sdesc_sw128(q0 + b * (kHU * 128) + 32 * kk), id_qk, (part | bb | kk) != 0);
+                        ptx::sdesc_sw128(q0 + b * (kHU * 128) + 32 * kk), id_q1, (part | bb | kk) != 0);
           }
       } else {
-        // S_b^T = C_b . (Qhi_b + Qlo_b)^T, 32 dims per step (plain E4M3: one sum over the blocks)
+        // S_b^T = C_b . [Qhi_b; Qlo_b]^T, 32 dims per step (plain E4M3: one sum over the blocks)
+        const bool split = F::split_terms(kHU, part);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
-            ptx::mma_f8(T0 + (F::kDs ? kHU * part : 0), ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][part]) + 32 * kk),
-                        ptx::sdesc_sw128(q0 + (2 * part + term) * (kHU * 128) + 32 * kk), id_qk,
-                        F::kDs ? (kk | term) != 0 : (part | kk | term) != 0);
+          for (int term = 0; term < (split ? 1 : 2); ++term)
+            ptx::mma_f8(T0 + F::col_block(kHU, part), ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][part]) + 32 * kk),
+                        ptx::sdesc_sw128(q0 + (2 * part + term) * (kHU * 128) + 32 * kk), split ? id_q2 : id_q1,
+                        F::kDs ? (kk | term) != 0 : (part | kk) != 0);
       }
       if (part < kParts - 1) return;
       const uint32_t pe0 = ptx::smem_u32(S.pe[buf]);
@@ -574,14 +614,12 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         if constexpr (F::kPlain) {
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-              ptx::mma_f8(T0, ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + term * (kHU * 128) + 32 * kk), id_qk, true);
+            ptx::mma_f8(T0, ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk), id_q2, true);
         } else {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_bf(T0 + (F::kDs ? 4 * kHU : 0), ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk), id_pe,
-                        F::kBf || kk > 0);
+            ptx::mma_bf(T0 + (F::kDs ? F::col_rope(kHU) : 0), ptx::sdesc_sw128(pe0 + 32 * kk), ptx::sdesc_sw128(qp + 32 * kk),
+                        id_pe, F::kBf || kk > 0);
         }
       }
       ptx::mma_commit(&S.s_full);
@@ -719,9 +757,6 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       for (int jj = 0; jj < s.ne; ++jj, ++k) {
         const int buf = k % kBufs;
         ok = ok && warp_wait(&S.full[buf][kParts - 1], (k / kBufs) & 1, abort) && warp_wait(&S.s_full, k & 1, abort);
-        if (!ok) *abort = 1;
-        ok = softmax_all(ok);
-        if (!ok) break;
         ptx::tc_fence_after();
         const int4 rr = S.rows[k & 3];
         const int prow = row & 63;
@@ -734,28 +769,43 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           scv[1] = valid ? f.y : 0.f;
           scv[2] = valid ? f.z : 0.f;
           scv[3] = valid ? f.w : 0.f;
-          uint32_t v[5][kHT];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tmem_ldn(T0 + kHU * b + kHT * hq + lane_off, v[b]);
-          if (P.rope_dim) tmem_ldn(T0 + kHU * 4 + kHT * hq + lane_off, v[4]);
-          ptx::tmem_wait_ld();
+          for (int h = 0; h < kHT; ++h) z[h] = 0.f;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) ptx::reg_fence(v[b]);
-          if (P.rope_dim) ptx::reg_fence(v[4]);
+          for (int b = 0; b < 4; b += 2) {   // two blocks at a time: their loads overlap
+            uint32_t v[2][2 * kHT], w[kHT];
+            tmem_ldn(T0 + F::col_block(kHU, b) + 2 * kHT * hq + lane_off, v[0]);
+            if (F::split_terms(kHU, b + 1)) tmem_ldn(T0 + F::col_block(kHU, b + 1) + 2 * kHT * hq + lane_off, v[1]);
+            else tmem_ldn(T0 + F::col_block(kHU, b + 1) + kHT * hq + lane_off, w);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence(v[0]);
+            if (F::split_terms(kHU, b + 1)) ptx::reg_fence(v[1]);
+            else ptx::reg_fence(w);
 #pragma unroll
-          for (int h = 0; h < kHT; ++h) {
-            z[h] = 0.f;
+            for (int h = 0; h < kHT; ++h) {
+              z[h] = fmaf(scv[b], __uint_as_float(v[0][h]) + __uint_as_float(v[0][kHT + h]), z[h]);
+              z[h] = fmaf(scv[b + 1],
+                          F::split_terms(kHU, b + 1) ? __uint_as_float(v[1][h]) + __uint_as_float(v[1][kHT + h])
+                                                     : __uint_as_float(w[h]),
+                          z[h]);
+            }
+          }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) z[h] = fmaf(scv[b], __uint_as_float(v[b][h]), z[h]);
-            z[h] *= qsh[h];
-            if (P.rope_dim) z[h] += __uint_as_float(v[4][h]);
+          for (int h = 0; h < kHT; ++h) z[h] *= qsh[h];
+          if (P.rope_dim) {
+            uint32_t v[kHT];
+            tmem_ldn(T0 + F::col_rope(kHU) + kHT * hq + lane_off, v);
+            ptx::tmem_wait_ld(v);
+#pragma unroll
+            for (int h = 0; h < kHT; ++h) z[h] += __uint_as_float(v[h]);
           }
         } else {
-          uint32_t v[kHT];
-          tmem_ldn(T0 + kHT * hq + lane_off, v);
+          uint32_t v[F::kBf ? kHT : 2 * kHT];
+          tmem_ldn(T0 + (F::kBf ? kHT : 2 * kHT) * hq + lane_off, v);
           ptx::tmem_wait_ld(v);
 #pragma unroll
-          for (int h = 0; h < kHT; ++h) z[h] = __uint_as_float(v[h]) * qsh[h];
+          for (int h = 0; h < kHT; ++h)
+            z[h] = (__uint_as_float(v[h]) + (F::kBf ? 0.f : __uint_as_float(v[F::kBf ? h : kHT + h]))) * qsh[h];
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -777,32 +827,38 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
             ebi[b] = __int_as_float((127 + e) << 23);
           }
         }
-        // This key's weights 2^(z - M_h) scale_b must stay within E4M3's 448.
-        // A weight above the cap, or a head without M_h yet, sends the
+        // This key's weights 2^(z - M_h) scale_b must stay within E4M3's 448:
+        // with lk the logarithm of its largest scale, z + lk - M_h bounds
+        // them.  A bound above the cap, or a head without M_h yet, sends the
         // quarter's four warps through the exact update (a vote: rare after
         // the first tile).  bf16: no scales; M_h only keeps 2^(z - M_h) within
         // 2^16.
-        float lk = 0.f;
+        float lk = 0.f, rk = 1.f;   // and rk = 2^-lk
         if constexpr (F::kDs) {
 #pragma unroll
           for (int b = 0; b < 4; ++b) scv[b] *= ebf[b];
           lk = lg2(fmaxf(fmaxf(fmaxf(scv[0], scv[1]), fmaxf(scv[2], scv[3])), 0x1p-60f));
+          rk = ex2(-lk);
+#pragma unroll
+          for (int h = 0; h < kHT; ++h) z[h] += lk;
         }
         constexpr float kCap = F::kBf ? 16.f : kLog2Cap, kHead = F::kBf ? 0.f : kLog2Head;
         bool need = false;
 #pragma unroll
-        for (int h = 0; h < kHT; ++h) need = need || (z[h] != -INFINITY && !(z[h] - M[h] + lk <= kCap));
-        need = group_any(hq, need);
+        for (int h = 0; h < kHT; ++h) need = need || (z[h] != -INFINITY && !(z[h] - M[h] <= kCap));
+        need = group_any(hq, need || !ok);
         float f[kHT];
         bool any = false;
         if (need) {
+          ok = !group_any(hq, !ok);   // a wait that gave up ends the quarter's warps together
+          if (!ok) break;
           // A head whose largest weight of this tile passes the cap takes the
           // integer M_h that puts it in (56, 112]: headroom of 4 for later
           // tiles, and the dominant weights keep all eight bits.  O and the
           // row sums scale by 2^(M_old - M_new), exactly.
 #pragma unroll
           for (int h = 0; h < kHT; ++h) {
-            const float x = ptx::warp_max_f32(z[h] + lk);
+            const float x = ptx::warp_max_f32(z[h]);
             if (lane == 0) S.xmax[hq][q4][h] = x;
           }
           group_sync(hq);
@@ -828,18 +884,18 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           ok = warp_wait(&S.pv_done, (k - 1) & 1, abort);
           if (!ok) {
             *abort = 1;
-            continue;   // the next softmax_all ends every softmax warp
+            continue;   // the next vote ends the quarter's warps
           }
           if (any) {
             ptx::tc_fence_after();
 #pragma unroll 1
-            for (int b = 0; b < 8; ++b) {   // (block, term): this thread's latent dim, this quarter's heads
-              uint32_t ov[kHT];
-              const uint32_t a = T0 + kColO + kHU * b + kHT * hq + lane_off;
+            for (int b = 0; b < 4; ++b) {   // this thread's latent dim of block b, this quarter's heads
+              uint32_t ov[2 * kHT];
+              const uint32_t a = T0 + kColO + 2 * kHU * b + 2 * kHT * hq + lane_off;
               tmem_ldn(a, ov);
               ptx::tmem_wait_ld(ov);
 #pragma unroll
-              for (int h = 0; h < kHT; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * f[h]);
+              for (int h = 0; h < 2 * kHT; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * f[h % kHT]);
               tmem_stn(a, ov);
             }
             ptx::tmem_wait_st();
@@ -847,51 +903,49 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         }
 #pragma unroll
         for (int h = 0; h < kHT; ++h) {
-          const float p = z[h] == -INFINITY ? 0.f : ex2(z[h] - M[h]);
-          lrow[h] += p;
+          const float p = z[h] == -INFINITY ? 0.f : ex2(z[h] - M[h]);   // times this key's largest scale
+          lrow[h] = fmaf(p, rk, lrow[h]);
           z[h] = p;
         }
-        // weights as [high | low] terms, keys by heads
+        // weights: keys by [high | low] terms of each head quarter
         if constexpr (F::kBf) {
-          const uint32_t pb = ptx::smem_u32(S.pb[0]) + (row >> 3) * kGroupBf<kHU> + (row & 7) * 16;
+          const uint32_t pb = ptx::smem_u32(S.pb[0]) + (row >> 3) * kGroupBf<kHU> + (row & 7) * 16 + hq * (kHT / 4) * 128;
+          uint32_t hi[kHT / 2], lo[kHT / 2];
 #pragma unroll
-          for (int i = 0; i < kHT / 4; ++i) {
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const __nv_bfloat162 hv = __floats2bfloat162_rn(z[4 * i + 2 * c], z[4 * i + 2 * c + 1]);
-              const float2 hf = __bfloat1622float2(hv);
-              const __nv_bfloat162 lv = __floats2bfloat162_rn(z[4 * i + 2 * c] - hf.x, z[4 * i + 2 * c + 1] - hf.y);
-              hi[c] = *reinterpret_cast<const uint32_t*>(&hv);
-              lo[c] = *reinterpret_cast<const uint32_t*>(&lv);
-            }
-            const int hd = kHT * hq + 4 * i;   // first of four heads: 16-B chunk hd / 8
-            st_v2(pb + (hd >> 3) * 128 + (hd & 7) * 2, hi[0], hi[1]);
-            st_v2(pb + (kHU / 8 + (hd >> 3)) * 128 + (hd & 7) * 2, lo[0], lo[1]);
+          for (int i = 0; i < kHT / 2; ++i) {
+            const __nv_bfloat162 hv = __floats2bfloat162_rn(z[2 * i], z[2 * i + 1]);
+            const float2 hf = __bfloat1622float2(hv);
+            const __nv_bfloat162 lv = __floats2bfloat162_rn(z[2 * i] - hf.x, z[2 * i + 1] - hf.y);
+            hi[i] = *reinterpret_cast<const uint32_t*>(&hv);
+            lo[i] = *reinterpret_cast<const uint32_t*>(&lv);
+          }
+          if constexpr (kHT == 4) {
+            st_v4(pb, hi[0], hi[1], lo[0], lo[1]);
+          } else {
+            st_v4(pb, hi[0], hi[1], hi[2], hi[3]);
+            st_v4(pb + 128, lo[0], lo[1], lo[2], lo[3]);
           }
         } else {
-          const int hd = kHT * hq;   // 16-B chunk hd / 16
-          const uint32_t off = (row >> 3) * (kHU * 16) + (row & 7) * 16 + (hd >> 4) * 128 + (hd & 15);
+          __half2 p2[kHT / 2];
+#pragma unroll
+          for (int i = 0; i < kHT / 2; ++i) p2[i] = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
+          const uint32_t off = (row >> 3) * (kHU * 16) + (row & 7) * 16 + ((2 * kHT * hq) >> 4) * 128 + ((2 * kHT * hq) & 15);
 #pragma unroll
           for (int b = 0; b < F::kSets; ++b) {
             const uint32_t pb = off + (Sm::kOverlay && b >= 2 ? ptx::smem_u32(S.pe[buf]) + (b - 2) * Sm::kSetBytes
                                                               : ptx::smem_u32(S.pb[Sm::kOverlay ? b & 1 : b]));
+            const __half2 sc2 = __float2half2_rn(F::kDs ? scv[b] * rk : 1.f);   // at most 1
             uint32_t hi[kHT / 4], lo[kHT / 4];
 #pragma unroll
             for (int i = 0; i < kHT / 4; ++i) {
               uint32_t h01, l01, h23, l23;
-              split2_e4m3x2(z[4 * i] * scv[b], z[4 * i + 1] * scv[b], h01, l01);
-              split2_e4m3x2(z[4 * i + 2] * scv[b], z[4 * i + 3] * scv[b], h23, l23);
+              split2_e4m3x2(F::kDs ? __hmul2_rn(p2[2 * i], sc2) : p2[2 * i], h01, l01);
+              split2_e4m3x2(F::kDs ? __hmul2_rn(p2[2 * i + 1], sc2) : p2[2 * i + 1], h23, l23);
               hi[i] = h01 | (h23 << 16);
               lo[i] = l01 | (l23 << 16);
             }
-            if constexpr (kHT == 4) {
-              st_b32(pb, hi[0]);
-              st_b32(pb + (kHU / 16) * 128, lo[0]);
-            } else {
-              st_v2(pb, hi[0], hi[1]);
-              st_v2(pb + (kHU / 16) * 128, lo[0], lo[1]);
-            }
+            if constexpr (kHT == 4) st_v2(pb, hi[0], lo[0]);
+            else st_v4(pb, hi[0], hi[1], lo[0], lo[1]);
           }
         }
         // A masked row may hold anything, and 0 x NaN is NaN in the product:
@@ -950,15 +1004,13 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        uint32_t hi[kHT], lo[kHT];
-        const uint32_t a = T0 + kColO + 2 * kHU * b + kHT * hq + lane_off;
-        tmem_ldn(a, hi);
-        tmem_ldn(a + kHU, lo);
-        ptx::tmem_wait_ld(hi, lo);
+        uint32_t ov[2 * kHT];
+        tmem_ldn(T0 + kColO + 2 * kHU * b + 2 * kHT * hq + lane_off, ov);
+        ptx::tmem_wait_ld(ov);
         const int dim = 128 * b + row;
 #pragma unroll
         for (int h = 0; h < kHT; ++h) {
-          const float o = (__uint_as_float(hi[h]) + __uint_as_float(lo[h])) * osc[h] * ebi[b];
+          const float o = (__uint_as_float(ov[h]) + __uint_as_float(ov[kHT + h])) * osc[h] * ebi[b];
           if (s.whole) {
             const __nv_bfloat16 r = __float2bfloat16_rn(o);
             P.out[(orow + kHT * hq + h) * SML_LATENT_DIM + dim] = *reinterpret_cast<const uint16_t*>(&r);
@@ -984,34 +1036,85 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
 
 // out = sum_i exp(lse_i - lse) O_i, lse = ln sum_i exp(lse_i) over the pieces
 // of one token that several CTAs hold.  One block per (CTA, head of its unit);
-// only the CTA after the one that begins a split token has something to join.
-__global__ void __launch_bounds__(128) paged_join_kernel(int H, int heads, PagedWs ws, uint16_t* __restrict__ out,
-                                                         float* __restrict__ lse) {
-  const int c = blockIdx.x, hl = blockIdx.y, g = c / ws.cpg;
-  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+// the CTAs that continue a token share its output dims, up to eight of them
+// 64 each, so that a token cut into many pieces is joined by many blocks.  The
+// weights of all pieces first, a thread each; then groups of threads add up
+// every kGroups-th piece, four loads in flight each.
+constexpr int kJoinThreads = 256, kMaxPieces = 1024;
+
+__global__ void __launch_bounds__(kJoinThreads)
+paged_join_kernel(int H, int heads, PagedWs ws, uint16_t* __restrict__ out, float* __restrict__ lse) {
+  __shared__ float wt[kMaxPieces];
+  __shared__ float red[kJoinThreads / 32], red2[kJoinThreads / 32];
+  __shared__ float4 sums[kJoinThreads];
+  const int c = blockIdx.x, hl = blockIdx.y, g = c / ws.cpg, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int4 rec = __ldcg(ws.join + c);
   if (rec.x < 0) return;
-  auto row = [&](int i) { return (size_t)((g * ws.cpg + i) * 2 + (i == rec.y)) * heads + hl; };
+  const int n = rec.z - rec.y + 1, idx = rec.w - rec.y - 1;   // pieces, and this block's place among the joiners
+  const int shares = n - 1 >= 8 ? 8 : n - 1 >= 4 ? 4 : n - 1 >= 2 ? 2 : 1;
+  if (idx >= shares) return;
+  auto row = [&](int i) { return (size_t)((g * ws.cpg + rec.y + i) * 2 + (i == 0)) * heads + hl; };
   float m = -INFINITY;
-  for (int i = rec.y; i <= rec.z; ++i) m = fmaxf(m, __ldcg(ws.part_lse + row(i)));
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-  for (int i = rec.y; i <= rec.z && m != -INFINITY; ++i) {
-    const float w = expf(__ldcg(ws.part_lse + row(i)) - m);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(ws.part_out + row(i) * SML_LATENT_DIM) + threadIdx.x);
-    den += w;
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  for (int i = tid; i < n; i += kJoinThreads) {
+    wt[i] = __ldcg(ws.part_lse + row(i));
+    m = fmaxf(m, wt[i]);
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  m = ptx::warp_max_f32(m);
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
+  float den = 0.f;
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float w = m == -INFINITY ? 0.f : expf(wt[i] - m);
+    wt[i] = w;
+    den += w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (lane == 0) red2[warp] = den;
+  __syncthreads();
+  den = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) den += red2[w];
+  const int cols = 128 / shares, groups = kJoinThreads / cols;   // columns of four dims
+  const int part = tid / cols, col = idx * cols + tid % cols;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = part; i0 < n; i0 += 4 * groups) {
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * groups;
+      v[u] = i < n ? __ldcg(reinterpret_cast<const float4*>(ws.part_out + row(i) * SML_LATENT_DIM) + col)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w = i0 + u * groups < n ? wt[i0 + u * groups] : 0.f;
+      o.x = fmaf(w, v[u].x, o.x);
+      o.y = fmaf(w, v[u].y, o.y);
+      o.z = fmaf(w, v[u].z, o.z);
+      o.w = fmaf(w, v[u].w, o.w);
+    }
+  }
+  sums[tid] = o;
+  __syncthreads();
+  if (part) return;
+  for (int i = 1; i < groups; ++i) {
+    const float4 v = sums[i * cols + tid];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
+  }
+  const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;   // NaN stays
   const size_t orow = (size_t)rec.x * H + g * heads + hl;
   const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(out + orow * SML_LATENT_DIM)[threadIdx.x] =
+  reinterpret_cast<uint2*>(out + orow * SML_LATENT_DIM)[col] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (threadIdx.x == 0) lse[orow] = den > 0.f ? m + logf(den) : -INFINITY;
+  if (tid == 0 && idx == 0) lse[orow] = den == 0.f ? -INFINITY : m + logf(den);
 }
 
 template <int kFmt, int kHU>
@@ -1022,7 +1125,8 @@ cudaError_t launch_unit(const CUtensorMap& rows, const CUtensorMap& scales, cons
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(P.ws.hg * P.ws.cpg), dim3(kThreads), smem, stream, 0, rows, scales, P);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_join_kernel, dim3(P.ws.hg * P.ws.cpg, kHU), dim3(128), 0, stream, 0, P.H, kHU, P.ws, P.out, P.lse);
+  return launch_pdl(paged_join_kernel, dim3(P.ws.hg * P.ws.cpg, kHU), dim3(kJoinThreads), 0, stream, 0, P.H, kHU, P.ws, P.out,
+                    P.lse);
 }
 
 template <int kFmt>
@@ -1037,7 +1141,8 @@ int paged_heads(const sml_problem& p) { return p.num_heads == 16 ? 16 : 32; }
 PagedWs paged_plan(const sml_problem& p) {
   PagedWs w = {};
   w.hg = p.num_heads / paged_heads(p);
-  w.cpg = device_sm_count() / w.hg > 0 ? device_sm_count() / w.hg : 1;
+  const int cpg = device_sm_count() / w.hg;
+  w.cpg = cpg < 1 ? 1 : cpg > kMaxPieces ? kMaxPieces : cpg;   // a token has at most cpg pieces
   return w;
 }
 
@@ -1059,6 +1164,7 @@ cudaError_t launch_paged_mla(const sml_problem& p, const uint16_t* q, const sml_
   P.vis_len = p.vis_len;
   P.ssmax_len = p.ssmax_len;
   P.q = q;
+  P.latent = static_cast<const uint8_t*>(latent.base);
   P.latent_pages = latent.num_pages;
   P.latent_scale = latent.format == SML_LATENT_E4M3 ? latent.scale : 1.f;
   P.sel = sel;

@@ -75,7 +75,7 @@ struct MlaWs {
 // partial slots and are joined by the merge: slot 0 for a piece that does not
 // begin its token, slot 1 for one that does.
 struct PagedWs {
-  int4* join;          // [ctas] {token, first CTA, last CTA} of the token to join at this CTA, token -1: none
+  int4* join;          // [ctas] {token, its first CTA, its last, this one} of the token that a CTA continues; token -1: none
   float* part_out;     // [ctas * 2 * heads per unit, 512]
   float* part_lse;     // [ctas * 2 * heads per unit]
   int hg;              // head groups

@@ -5,12 +5,13 @@ to the value):
 
 * the output is rounded to bf16 once: u |out|;
 * each softmax weight has at least 8 significant bits when it enters its product (u relative,
-  plus 2^-11 for one rounding to half precision on the way); the same weights unrounded are
-  summed for the denominator, so an output is off by at most (u + 2^-11) A, A = sum_i p_i |c_i|;
+  plus 2^-11 for each rounding to half precision on the way: of the weight, of the scale it is
+  multiplied with, and of the product); the same weights unrounded are summed for the
+  denominator, so an output is off by at most (u + 3 * 2^-11) A, A = sum_i p_i |c_i|;
 * a weight far below the largest keeps only an absolute error: half of E4M3's subnormal step
-  (2^-10) against a largest weight-times-scale of at least 28 (an output's keys share it within
-  the spread of their block scales, a factor 4 for these inputs): 2^-10 / 28 * 4 <= 2^-12.8 of
-  the largest p, times sum_i |c_i|;
+  (2^-10) in each of its two terms against a largest weight-times-scale of at least 28 (an
+  output's keys share it within the spread of their block scales, a factor 4 for these inputs):
+  2^-9 / 28 * 4 <= 2^-11.8 of the largest p, times sum_i |c_i|;
 * a logit is a sum in fp32 of up to 576 products: off by at most d = 576 * 2^-23 of the summed terms'
   size (2^-23, not 2^-24: the tensor cores may cut instead of round).  A softmax weight then moves by
   p_i |d_i - mean d| <= 2 d p_i (1 - p_i), the output by 2 d sum_i p_i (1 - p_i) |c_i|, and the
@@ -42,7 +43,7 @@ def expect(wl, layer_i, t, positions, n=None, nss=None):
     p = np.exp(scale * (q @ keys.T) - lse[:, None])
     A = p @ np.abs(c)
     d = 576 * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(keys).T).max(1)
-    tol = 2 * d[:, None] * ((p * (1 - p)) @ np.abs(c)) + U * np.abs(out) + (U + 2.0 ** -11) * A * 1.01 + 2.0 ** -12.8 * p.max(1)[:, None] * np.abs(c).sum(0)[None]
+    tol = 2 * d[:, None] * ((p * (1 - p)) @ np.abs(c)) + U * np.abs(out) + (U + 3 * 2.0 ** -11) * A * 1.01 + 2.0 ** -11.8 * p.max(1)[:, None] * np.abs(c).sum(0)[None]
     return out, lse, tol, d + 2.0 ** -20 * (1 + np.abs(lse))
 
 
