@@ -27,7 +27,6 @@ constexpr int kSoftmaxWarps = 16;        // warps 0-15
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kWarpQk = 16, kWarpPv = 17, kWarpLoad = 18;
 constexpr int kThreads = 608;
-constexpr int kAhead = 2;                // tiles between an L2 prefetch and the tile being loaded
 constexpr uint32_t kColO = 256;          // TMEM: logits from column 0, O from here
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,58 +63,66 @@ struct Tok {
   bool ok, len_bad;
 };
 
-// Request of token t: with equal query counts it is t B / T, which two loads
-// confirm; else a binary search.
-__device__ __forceinline__ int find_request(const Params& P, int t) {
-  const int guess = (int)((long long)t * P.B / P.T);
-  if (__ldg(P.cu_q + guess) <= t && t < __ldg(P.cu_q + guess + 1)) return guess;
-  return request_of(P.cu_q, P.B, t);
-}
-
+// Every load of a token's lengths in one round: with equal query counts its
+// request is t B / T, which the request's own offsets confirm; else a binary
+// search and a second round.
 __device__ __forceinline__ Tok token_at(const Params& P, int t) {
   Tok k;
-  k.r = find_request(P, t);
-  const Req rq = load_request(P.cu_q, P.ctx_len, k.r, P.T, P.max_ctx, P.max_pages, P.vis_len != nullptr);
-  k.ok = rq.ok && t >= rq.q0 && t - rq.q0 < rq.Q;
-  bool bad = false;
-  k.n = k.ok ? visible_len(P.vis_len, rq, t, &bad) : 0;
-  k.ok = k.ok && !bad;
-  if (!k.ok) k.n = 0;
-  k.nss = ssmax_len_of(P.ssmax_len, t, k.n);
-  k.lo = P.sel.window > 0 && k.n > P.sel.window ? k.n - P.sel.window : 0;
-  k.len_bad = false;
-  if (P.sel.blocks) {
-    const int len = k.ok ? __ldg(P.sel.blocks_len + t) : 0;
-    k.len_bad = len < 0 || len > P.sel.max_blocks;
-    k.np = max(0, min(len, P.sel.max_blocks));
-  } else {
-    k.np = (k.n + SML_PAGE_TOKENS - 1) / SML_PAGE_TOKENS - k.lo / SML_PAGE_TOKENS;
+  k.r = (int)((unsigned)((long long)t * P.B) / (unsigned)P.T);   // t, B, T <= 65535
+  Req rq = load_request(P.cu_q, P.ctx_len, k.r, P.T, P.max_ctx, P.max_pages, P.vis_len != nullptr);
+  const int vis = P.vis_len ? __ldg(P.vis_len + t) : 0, ssl = P.ssmax_len ? __ldg(P.ssmax_len + t) : 0;
+  const int len = P.sel.blocks ? __ldg(P.sel.blocks_len + t) : 0;
+  if (!(rq.q0 <= t && t - rq.q0 < rq.Q)) {
+    k.r = request_of(P.cu_q, P.B, t);
+    rq = load_request(P.cu_q, P.ctx_len, k.r, P.T, P.max_ctx, P.max_pages, P.vis_len != nullptr);
   }
+  k.ok = rq.ok && t >= rq.q0 && t - rq.q0 < rq.Q;
+  if (P.vis_len) {
+    k.ok = k.ok && vis >= 0 && vis <= rq.L;
+    k.n = k.ok ? vis : 0;
+  } else {
+    k.n = k.ok ? rq.L - rq.Q + (t - rq.q0) + 1 : 0;
+  }
+  k.nss = max(1, P.ssmax_len ? ssl : k.n);
+  k.lo = P.sel.window > 0 && k.n > P.sel.window ? k.n - P.sel.window : 0;
+  k.len_bad = P.sel.blocks && k.ok && (len < 0 || len > P.sel.max_blocks);
+  k.np = !P.sel.blocks ? (k.n + SML_PAGE_TOKENS - 1) / SML_PAGE_TOKENS - k.lo / SML_PAGE_TOKENS
+         : k.ok        ? max(0, min(len, P.sel.max_blocks))
+                       : 0;
   return k;
 }
 
 __device__ __forceinline__ int tiles_of(const Tok& k) { return max(1, (k.np + 1) / 2); }
 
-// Logical and physical page of the k-th page of token t (physical -1: masked,
-// and reported by the one thread that asks with report set).
-__device__ __forceinline__ int page_at(const Params& P, const Tok& tk, int t, int k, bool report, int* logical) {
-  *logical = 0;
-  if (k >= tk.np) return -1;
-  int lg = tk.lo / SML_PAGE_TOKENS + k;
+// Logical and physical page of the k-th and the l-th page of token t (physical
+// -1: masked, and reported where asked); the loads of both overlap.
+struct Page {
+  int lg, ph;
+};
+__device__ __forceinline__ void pages_at(const Params& P, const Tok& tk, int t, int k, bool report_k, Page& a, int l,
+                                         bool report_l, Page& b) {
+  const bool ka = k < tk.np, kb = l < tk.np;
+  a.lg = tk.lo / SML_PAGE_TOKENS + k;
+  b.lg = tk.lo / SML_PAGE_TOKENS + l;
+  bool va = ka, vb = kb;
   if (P.sel.blocks) {
-    lg = __ldg(P.sel.blocks + (size_t)t * P.sel.max_blocks + k);
-    if (lg < 0 || lg >= (tk.n + SML_PAGE_TOKENS - 1) / SML_PAGE_TOKENS) {
-      if (report) raise_fault(P.status, SML_FAULT_INDEX);
-      return -1;
-    }
+    const int32_t* list = P.sel.blocks + (size_t)t * P.sel.max_blocks;
+    const int all = (tk.n + SML_PAGE_TOKENS - 1) / SML_PAGE_TOKENS;
+    a.lg = ka ? __ldg(list + k) : 0;
+    b.lg = kb ? __ldg(list + l) : 0;
+    va = ka && a.lg >= 0 && a.lg < all;
+    vb = kb && b.lg >= 0 && b.lg < all;
+    if ((ka && !va && report_k) || (kb && !vb && report_l)) raise_fault(P.status, SML_FAULT_INDEX);
   }
-  *logical = lg;
-  const int ph = __ldg(P.block_table + (size_t)tk.r * P.max_pages + lg);
-  if (ph < 0 || ph >= P.latent_pages) {
-    if (report) raise_fault(P.status, SML_FAULT_PAGE);
-    return -1;
-  }
-  return ph;
+  const int32_t* table = P.block_table + (size_t)tk.r * P.max_pages;
+  a.ph = va ? __ldg(table + a.lg) : -1;
+  b.ph = vb ? __ldg(table + b.lg) : -1;
+  const bool pa = a.ph >= 0 && a.ph < P.latent_pages, pb = b.ph >= 0 && b.ph < P.latent_pages;
+  if ((va && !pa && report_k) || (vb && !pb && report_l)) raise_fault(P.status, SML_FAULT_PAGE);
+  if (!pa) a.ph = -1;
+  if (!pb) b.ph = -1;
+  if (!va) a.lg = 0;
+  if (!vb) b.lg = 0;
 }
 
 // This CTA's range of its head group's tiles, and the token it starts in.
@@ -129,8 +136,13 @@ struct PlanSmem {
   int t0;
 };
 
-__device__ __forceinline__ long long range_begin(long long total, int used, int i) { return total * i / used; }
-__device__ __forceinline__ int cta_of(long long total, int used, long long u) { return (int)(((u + 1) * used - 1) / total); }
+// a / b of non-negative numbers, in 32 bits where both fit (a 64-bit division
+// is a long routine, and several stand at the start of every CTA).
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ long long range_begin(long long total, int used, int i) { return div_ll(total * i, used); }
+__device__ __forceinline__ int cta_of(long long total, int used, long long u) { return (int)div_ll((u + 1) * used - 1, total); }
 
 template <int kN>
 __device__ Range plan_range(const Params& P, int gi, PlanSmem& S) {
@@ -154,8 +166,8 @@ __device__ Range plan_range(const Params& P, int gi, PlanSmem& S) {
     R.total += S.part[w];
   }
   // as few CTAs as give the same longest range
-  const long long most = (R.total + P.ws.cpg - 1) / P.ws.cpg;
-  R.used = (int)((R.total + most - 1) / most);
+  const long long most = div_ll(R.total + P.ws.cpg - 1, P.ws.cpg);
+  R.used = (int)div_ll(R.total + most - 1, most);
   R.ub = gi < R.used ? range_begin(R.total, R.used, gi) : 0;
   R.ue = gi < R.used ? range_begin(R.total, R.used, gi + 1) : 0;
   const long long first = before + upto - mine;   // first tile of token a
@@ -487,7 +499,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
   const uint32_t T0 = S.tmem_base;
   const Range R = plan_range<kThreads>(P, gi, S.plan);
   const int slot = (g * P.ws.cpg + gi) * 2;
-  if (threadIdx.x == 0) {
+  if (warp == kWarpPv && lane == 0) {
     // the token that this CTA continues, and the CTAs that hold it
     int4 rec = make_int4(-1, 0, 0, 0);
     if (gi < R.used && R.ub > R.tok0)
@@ -512,28 +524,25 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         if (!s.tk.ok) raise_fault(P.status, SML_FAULT_LENGTHS);
         if (s.tk.len_bad) raise_fault(P.status, SML_FAULT_TOPK_LEN);
       }
-      int ph = -1, lg = 0, phn = -1, lgn = 0;   // of page 2 (j0 + 16 i) + lane, and 32 pages on
+      Page pg = {0, -1}, pn = {0, -1};   // pages 2 (j0 + 16 i) + lane, and 32 on
       for (int jj = 0; jj < s.ne; ++jj, ++k) {
-        const int buf = k % kBufs, two = 2 * (jj & 15);
-        if (two == 0) {
-          if (jj == 0) {
-            ph = page_at(P, s.tk, s.t, 2 * s.j0 + lane, lane < 2 * s.ne, &lg);
-          } else {
-            ph = phn;
-            lg = lgn;
-          }
-          phn = page_at(P, s.tk, s.t, 2 * (s.j0 + jj) + 32 + lane, lane + 32 < 2 * (s.ne - jj), &lgn);
+        const int buf = k % kBufs, two = 2 * (jj & 15), k0 = 2 * (s.j0 + jj) + lane;
+        if (jj == 0) {
+          pages_at(P, s.tk, s.t, k0, lane < 2 * s.ne, pg, k0 + 32, lane + 32 < 2 * s.ne, pn);
+        } else if (two == 0) {
+          pg = pn;
+          Page none;
+          pages_at(P, s.tk, s.t, k0 + 32, lane + 32 < 2 * (s.ne - jj), pn, s.tk.np, false, none);
         }
-        // The tile after next goes to L2 now, so that its loads, issued when a
-        // buffer is free, find it there.  One head group asks for all.
-        if (g == 0 && jj + kAhead < s.ne) {
-          const int i = two + 2 * kAhead;
-          const int a0 = __shfl_sync(0xffffffffu, i < 32 ? ph : phn, i & 31), a1 = __shfl_sync(0xffffffffu, i < 32 ? ph : phn, (i + 1) & 31);
-          const int pg = lane == 0 ? a0 : a1;
-          if (lane < 2 && pg >= 0) ptx::bulk_prefetch_l2(P.latent + (size_t)pg * F::kPageBytes, F::kPageBytes);
+        const int p0 = __shfl_sync(0xffffffffu, pg.ph, two), p1 = __shfl_sync(0xffffffffu, pg.ph, two + 1);
+        const int l0 = __shfl_sync(0xffffffffu, pg.lg, two), l1 = __shfl_sync(0xffffffffu, pg.lg, two + 1);
+        // While the tile's buffer is still in use its pages go to L2 (one head
+        // group asks for all): 32 contexts of 8K to 64K tokens take 148 us, 158
+        // without; two tiles ahead 153, four 207.
+        if (g == 0 && k >= kBufs && lane < 2) {
+          const int ph = lane == 0 ? p0 : p1;
+          if (ph >= 0) ptx::bulk_prefetch_l2(P.latent + (size_t)ph * F::kPageBytes, F::kPageBytes);
         }
-        const int p0 = __shfl_sync(0xffffffffu, ph, two), p1 = __shfl_sync(0xffffffffu, ph, two + 1);
-        const int l0 = __shfl_sync(0xffffffffu, lg, two), l1 = __shfl_sync(0xffffffffu, lg, two + 1);
         const uint32_t pages = (p0 >= 0) + (p1 >= 0);
         // The last part brings the scales and the RoPE keys: with 32 heads the
         // RoPE keys' place holds the weights of the last two parts until then.
@@ -555,8 +564,8 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
             ptx::mbar_arrive_expect_tx(bar, pages * (last ? last_bytes : kPartBytes));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const int pg = half ? p1 : p0, y = pg * SML_PAGE_TOKENS, off = half * SML_PAGE_TOKENS * 128;
-              if (pg < 0) continue;
+              const int ph = half ? p1 : p0, y = ph * SML_PAGE_TOKENS, off = half * SML_PAGE_TOKENS * 128;
+              if (ph < 0) continue;
 #pragma unroll
               for (int b = 0; b < kPartBlocks; ++b)
                 ptx::tma_load_2d(S.lat[buf][part * kPartBlocks + b] + off, &row_map, bar, 128 * (part * kPartBlocks + b), y);
