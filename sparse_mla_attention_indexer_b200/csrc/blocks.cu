@@ -105,11 +105,15 @@ Batch batch_of(const sml_problem& p, int32_t* status) {
                p.cu_q,         p.ctx_len,    p.block_table, p.vis_len, p.ssmax_len, status};
 }
 
-// Request and visible length (0 when the lengths are bad) of token t.
+// Request and visible length (0 when the lengths are bad) of token t: with
+// equal query counts its request is t B / T, else a binary search finds it.
 __device__ __forceinline__ int visible_of(const Batch& b, int t, int* r, bool* bad) {
-  const int guess = (int)((long long)t * b.B / b.T);
-  *r = __ldg(b.cu_q + guess) <= t && t < __ldg(b.cu_q + guess + 1) ? guess : request_of(b.cu_q, b.B, t);
-  const Req rq = load_request(b.cu_q, b.ctx_len, *r, b.T, b.max_ctx, b.max_pages, b.vis_len != nullptr);
+  *r = (int)((unsigned)((long long)t * b.B) / (unsigned)b.T);
+  Req rq = load_request(b.cu_q, b.ctx_len, *r, b.T, b.max_ctx, b.max_pages, b.vis_len != nullptr);
+  if (!(rq.q0 <= t && t - rq.q0 < rq.Q)) {
+    *r = request_of(b.cu_q, b.B, t);
+    rq = load_request(b.cu_q, b.ctx_len, *r, b.T, b.max_ctx, b.max_pages, b.vis_len != nullptr);
+  }
   *bad = !(rq.ok && t >= rq.q0 && t - rq.q0 < rq.Q);
   if (*bad) return 0;
   const int n = visible_len(b.vis_len, rq, t, bad);
@@ -117,57 +121,218 @@ __device__ __forceinline__ int visible_of(const Batch& b, int t, int* r, bool* b
 }
 
 // ---- block scores ---------------------------------------------------------------
-// One CTA per (token, 32 blocks); eight threads per block, eight heads each.
-constexpr int kScoreThreads = 256, kScoreBlocks = 32;
+// A CTA scores one tile of 128 blocks for up to kChunk consecutive tokens: the
+// blocks' keys are gathered once per request into shared memory (K-major rows
+// of 128 B, 128-B swizzle), then for each token the 64 x 128 query comes by
+// TMA and one D[128 blocks, 64 heads] = K Q^T runs on kind::f8f6f4 (exact E4M3
+// products, fp32 sums in TMEM).  Warps 0-3 gather the keys and reduce D over
+// the heads (thread = block); warp 4 loads queries up to four ahead and issues the
+// MMAs, so the product of the next token overlaps the reduction of the last.
+constexpr int kTileBlocks = 128, kChunk = 64, kEpiThreads = 128, kScoreThreads = kEpiThreads + 32;
+constexpr int kQBufs = 4;
+constexpr int kQueryBytes = SML_INDEX_HEADS * SML_INDEX_DIM;
 
-__global__ void __launch_bounds__(kScoreThreads)
-block_scores_kernel(Batch b, const uint8_t* __restrict__ iq8, const float* __restrict__ iq_scale,
+struct __align__(1024) ScoreSmem {
+  uint8_t key[kTileBlocks * SML_INDEX_DIM];
+  uint8_t q[kQBufs][kQueryBytes];
+  __align__(16) float w[kQBufs][SML_INDEX_HEADS];
+  int nb[kChunk], req[kChunk];   // of the CTA's tokens: candidate blocks, request
+  float fac[kChunk];             // and query scale times SSMax factor
+  uint64_t q_full[kQBufs], acc_full[2], acc_free[2], key_full, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
+}
+// AND of a flag over the epilogue warps (named barrier 1).
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(kEpiThreads)
+      : "memory");
+  return r != 0;
+}
+
+__global__ void __launch_bounds__(kScoreThreads, 4)
+block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk, const float* __restrict__ iq_scale,
                     const float* __restrict__ iw, const uint8_t* __restrict__ block, long long rows,
                     float* __restrict__ scores) {
-  __shared__ __half q[SML_INDEX_HEADS][SML_INDEX_DIM + 2];
-  __shared__ float key[kScoreBlocks][SML_INDEX_DIM + 1];
-  ptx::griddep_wait();
-  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
-  const int t = blockIdx.x, tid = threadIdx.x;
-  int r;
-  bool bad;
-  const int n = visible_of(b, t, &r, &bad), nb = n > 0 ? (n - 1) / SML_PAGE_TOKENS : 0;
-  if (bad && blockIdx.y == 0 && tid == 0) raise_fault(b.status, SML_FAULT_LENGTHS);
-  if ((int)blockIdx.y * kScoreBlocks >= nb) return;
-  for (int i = tid; i < SML_INDEX_HEADS * SML_INDEX_DIM / 2; i += kScoreThreads) {
-    const float2 v = e4m3x2_f(reinterpret_cast<const uint16_t*>(iq8 + (size_t)t * SML_INDEX_HEADS * SML_INDEX_DIM)[i]);
-    q[2 * i / SML_INDEX_DIM][2 * i % SML_INDEX_DIM] = __float2half(v.x);
-    q[2 * i / SML_INDEX_DIM][2 * i % SML_INDEX_DIM + 1] = __float2half(v.y);
+  extern __shared__ uint8_t raw[];
+  ScoreSmem& S = *reinterpret_cast<ScoreSmem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = blockIdx.y * chunk, nt = min(chunk, b.T - t0), j0 = blockIdx.x * kTileBlocks;
+  if (tid == 0) {
+    for (int i = 0; i < kQBufs; ++i) ptx::mbar_init(&S.q_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&S.acc_full[i], 1);
+      ptx::mbar_init(&S.acc_free[i], 4);
+    }
+    ptx::mbar_init(&S.key_full, 4);
+    ptx::mbar_init(&S.drain, 1);
+    S.abort = 0;
+    ptx::fence_mbar_init();
   }
-  const float c = b.ssmax ? b.s_index * logf((float)ssmax_len_of(b.ssmax_len, t, n)) : 1.f;
-  for (int j0 = blockIdx.y * kScoreBlocks; j0 < nb; j0 += gridDim.y * kScoreBlocks) {
-    __syncthreads();
-    const int j = j0 + tid / 8, part = tid % 8;
-    const int pg = j < nb ? __ldg(b.block_table + (size_t)r * b.max_pages + j) : -1;
-    const bool there = pg >= 0 && pg < rows;
-    const uint8_t* src = block + (size_t)(there ? pg / SML_PAGE_TOKENS : 0) * SML_INDEX_PAGE_BYTES;
-    const int row = there ? pg % SML_PAGE_TOKENS : 0;
+  ptx::griddep_wait();
+  if (tid == 0) ptx::griddep_launch_dependents();
+  bool any = false;
+  if (tid < nt) {
+    int r;
+    bool bad;
+    const float sq = __ldg(iq_scale + t0 + tid);
+    const int ssl = b.ssmax_len ? __ldg(b.ssmax_len + t0 + tid) : 0;
+    const int n = visible_of(b, t0 + tid, &r, &bad), nb = n > 0 ? (n - 1) / SML_PAGE_TOKENS : 0;
+    if (bad && blockIdx.x == 0) raise_fault(b.status, SML_FAULT_LENGTHS);
+    S.nb[tid] = nb;
+    S.req[tid] = r;
+    S.fac[tid] = sq * (b.ssmax ? b.s_index * logf((float)max(1, b.ssmax_len ? ssl : n)) : 1.f);
+    any = nb > j0;
+  }
+  if (!__syncthreads_or(any)) return;   // no token of the CTA has candidates in this tile
+  if (warp == 4) {
+    ptx::tmem_alloc(&S.tmem_base, 128);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  volatile int* abort = &S.abort;
+  const uint32_t T0 = S.tmem_base;
+  if (warp == 4) {
+    // ---- queries and products; tokens k = 0, 1, ... of those with candidates here ----
+    constexpr uint32_t id = ptx::idesc_f16(SML_INDEX_HEADS, 0, 0, 0);
+    const uint32_t key0 = ptx::smem_u32(S.key), q0 = ptx::smem_u32(S.q[0]);
+    auto next = [&](int i) {
+      while (i < nt && S.nb[i] <= j0) ++i;
+      return i;
+    };
+    int at = next(0), loaded = 0;   // the next token to load, and loads so far
+    auto load = [&]() {
+      if (at >= nt) return;
+      if (lane == 0) {
+        const int buf = loaded % kQBufs;
+        ptx::mbar_arrive_expect_tx(&S.q_full[buf], kQueryBytes + SML_INDEX_HEADS * 4);
+        ptx::tma_load_2d(S.q[buf], &qmap, &S.q_full[buf], 0, (t0 + at) * SML_INDEX_HEADS);
+        ptx::bulk_load(S.w[buf], iw + (size_t)(t0 + at) * SML_INDEX_HEADS, SML_INDEX_HEADS * 4, &S.q_full[buf]);
+      }
+      __syncwarp();
+      ++loaded;
+      at = next(at + 1);
+    };
+#pragma unroll 1
+    for (int i = 0; i < kQBufs; ++i) load();
+    bool ok = true;
+    int k = 0, runs = 0, last = -1;
+    for (int i = next(0); i < nt && ok; i = next(i + 1), ++k) {
+      if (S.req[i] != last) {
+        ok = warp_wait(&S.key_full, runs & 1, abort);
+        last = S.req[i];
+        ++runs;
+      }
+      if (ok && k >= 2) {
+        // token k - 2 is reduced: its D is free, and its query and weights make
+        // room for token k + 2
+        ok = warp_wait(&S.acc_free[k & 1], ((k >> 1) - 1) & 1, abort);
+        if (ok && loaded == k + 2) load();
+      }
+      ok = ok && warp_wait(&S.q_full[k % kQBufs], (k / kQBufs) & 1, abort);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 v = e4m3x2_f(reinterpret_cast<const uint16_t*>(src + row * SML_INDEX_DIM + 16 * part)[i]);
-      key[tid / 8][16 * part + 2 * i] = v.x;
-      key[tid / 8][16 * part + 2 * i + 1] = v.y;
+        for (int kk = 0; kk < SML_INDEX_DIM / 32; ++kk)
+          ptx::mma_f8(T0 + (k & 1) * SML_INDEX_HEADS, ptx::sdesc_sw128(key0 + 32 * kk),
+                      ptx::sdesc_sw128(q0 + (k % kQBufs) * kQueryBytes + 32 * kk), id, kk > 0);
+        ptx::mma_commit(&S.acc_full[k & 1]);
+      }
+      __syncwarp();
     }
-    __syncthreads();
-    float sum = 0.f;
-    for (int h = part; h < SML_INDEX_HEADS; h += 8) {
-      float dot = 0.f;
-#pragma unroll 16
-      for (int d = 0; d < SML_INDEX_DIM; ++d) dot = fmaf(__half2float(q[h][d]), key[tid / 8][d], dot);
-      sum = fmaf(iw[(size_t)t * SML_INDEX_HEADS + h], fmaxf(dot, 0.f), sum);
-    }
+    if (!ok) *abort = 1;
+    for (int i = max(0, loaded - kQBufs); i < loaded; ++i)
+      ptx::mbar_wait(&S.q_full[i % kQBufs], (i / kQBufs) & 1, nullptr, 100000u);
+    if (ptx::elect_one()) ptx::mma_commit(&S.drain);
+    __syncwarp();
+    ptx::mbar_wait(&S.drain, 0, nullptr, 100000u);
+    __syncwarp();
+  } else {
+    // ---- keys, then the reduction over the heads ----
+    const int j = j0 + tid;
+    const uint32_t dst = ptx::smem_u32(S.key) + (tid >> 3) * 1024 + (tid & 7) * 128;
+    bool ok = true, there = false;
+    float sb = 0.f;
+    int k = 0, last = -1;
+    for (int i = 0; i < nt; ++i) {
+      if (S.nb[i] <= j0) continue;
+      if (S.req[i] != last) {
+        // Every product with the last request's keys is done: each was waited
+        // for below.  Blocks past the request's last candidate hold zeros.
+        last = S.req[i];
+        int most = S.nb[i];
+        for (int x = i + 1; x < nt && S.req[x] == last; ++x) most = max(most, S.nb[x]);
+        const int pg = j < most ? __ldg(b.block_table + (size_t)last * b.max_pages + j) : -1;
+        there = pg >= 0 && pg < rows;
+        if (j < most && !there) raise_fault(b.status, SML_FAULT_PAGE);
+        const uint8_t* src = block + (size_t)(there ? pg / SML_PAGE_TOKENS : 0) * SML_INDEX_PAGE_BYTES;
+        const int row = there ? pg % SML_PAGE_TOKENS : 0;
+        sb = __ldcg(reinterpret_cast<const float*>(src + SML_PAGE_TOKENS * SML_INDEX_DIM) + row);
+        uint4 v[8];
 #pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (part == 0 && j < nb) {
-      const float sb = reinterpret_cast<const float*>(src + SML_PAGE_TOKENS * SML_INDEX_DIM)[row];
-      if (!there) raise_fault(b.status, SML_FAULT_PAGE);
-      scores[(size_t)t * b.max_pages + j] = there ? sum * (__ldg(iq_scale + t) * c) * sb : NAN;
+        for (int c = 0; c < 8; ++c)
+          v[c] = there ? __ldcg(reinterpret_cast<const uint4*>(src + row * SML_INDEX_DIM) + c) : make_uint4(0, 0, 0, 0);
+        ok = epi_all(ok);
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((c ^ (tid & 7)) << 4)), "r"(v[c].x),
+                       "r"(v[c].y), "r"(v[c].z), "r"(v[c].w)
+                       : "memory");
+        ptx::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.key_full);
+      }
+      const int acc = k & 1;
+      ok = ok && warp_wait(&S.q_full[k % kQBufs], (k / kQBufs) & 1, abort) && warp_wait(&S.acc_full[acc], (k >> 1) & 1, abort);
+      if (!ok) {
+        *abort = 1;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t d = T0 + ((uint32_t)(32 * warp) << 16) + acc * SML_INDEX_HEADS;
+      uint32_t v0[32], v1[32];
+      ptx::tmem_ld32(d, v0);
+      ptx::tmem_ld32(d + 32, v1);
+      ptx::tmem_wait_ld(v0, v1);
+      const float4* w = reinterpret_cast<const float4*>(S.w[k % kQBufs]);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 wa = w[c], wb = w[8 + c];
+        s[0] = fmaf(wa.x, fmaxf(__uint_as_float(v0[4 * c]), 0.f), s[0]);
+        s[1] = fmaf(wa.y, fmaxf(__uint_as_float(v0[4 * c + 1]), 0.f), s[1]);
+        s[2] = fmaf(wa.z, fmaxf(__uint_as_float(v0[4 * c + 2]), 0.f), s[2]);
+        s[3] = fmaf(wa.w, fmaxf(__uint_as_float(v0[4 * c + 3]), 0.f), s[3]);
+        s[0] = fmaf(wb.x, fmaxf(__uint_as_float(v1[4 * c]), 0.f), s[0]);
+        s[1] = fmaf(wb.y, fmaxf(__uint_as_float(v1[4 * c + 1]), 0.f), s[1]);
+        s[2] = fmaf(wb.z, fmaxf(__uint_as_float(v1[4 * c + 2]), 0.f), s[2]);
+        s[3] = fmaf(wb.w, fmaxf(__uint_as_float(v1[4 * c + 3]), 0.f), s[3]);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.acc_free[acc]);   // D and the weights have been read
+      if (j < S.nb[i])
+        scores[(size_t)(t0 + i) * b.max_pages + j] = there ? ((s[0] + s[1]) + (s[2] + s[3])) * S.fac[i] * sb : NAN;
+      ++k;
     }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && S.abort) raise_fault(b.status, SML_FAULT_TIMEOUT);
+  if (warp == 4) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(S.tmem_base, 128);
   }
 }
 
@@ -179,18 +344,21 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// One CTA per token: the k-th largest key of the row by four rounds of an 8-bit
-// histogram, then one ordered pass that keeps every larger key and the first
-// of the equal ones.  A row is read five times, from L1/L2 after the first.
-constexpr int kTopThreads = 512;
+// One CTA per token; thread i owns the row's entries [i c, i c + c), so that one
+// scan over the threads gives every kept entry its place in ascending order.
+// The threshold is the k-th largest key, by up to four rounds of an 8-bit
+// histogram that every warp scans for itself; a round whose digit holds exactly
+// the keys still wanted is the last.  kReg > 0: rows of up to kReg entries a
+// thread, read once into registers; 0: rows of any length, read from L1/L2 in
+// every round.
+constexpr int kTopThreads = 1024;
 
+template <int kReg>
 __global__ void __launch_bounds__(kTopThreads)
 block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __restrict__ blocks,
                   int32_t* __restrict__ blocks_len) {
-  __shared__ int hist[256];
-  __shared__ int warp_take[kTopThreads / 32], warp_tie[kTopThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ int hist[4][256];   // one per round, so that no round waits to clear another's
+  __shared__ int2 part[kTopThreads / 32];
   ptx::griddep_wait();
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -212,53 +380,111 @@ block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __r
     return;
   }
   if (take == 0) return;
+  const int c = (nb + kTopThreads - 1) / kTopThreads, i0 = min(nb, tid * c), i1 = min(nb, i0 + c);
+  uint32_t reg[kReg > 0 ? kReg : 1];
+  if constexpr (kReg > 0) {
+#pragma unroll
+    for (int u = 0; u < kReg; ++u)
+      if (u < c) reg[u] = i0 + u < i1 ? order_key(__ldg(row + i0 + u)) : 0u;
+  }
+  // f(index, key) for every entry of this thread, in order
+  auto each = [&](auto&& f) {
+    if constexpr (kReg > 0) {
+#pragma unroll
+      for (int u = 0; u < kReg; ++u)
+        if (u < c && i0 + u < i1) f(i0 + u, reg[u]);
+    } else {
+      for (int i = i0; i < i1; ++i) f(i, order_key(__ldg(row + i)));
+    }
+  };
+  static_assert(kTopThreads == 4 * 256, "a thread clears one counter");
+  (&hist[0][0])[tid] = 0;
+  __syncthreads();
   uint32_t prefix = 0;   // the threshold key's leading bits found so far
   int need = take;       // keys still wanted among those that share them
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kTopThreads) hist[i] = 0;
+#pragma unroll 1
+  for (int round = 0; round < 4; ++round) {
+    const int shift = 24 - 8 * round;
+    int* h = hist[round];
+    each([&](int, uint32_t key) {
+      if (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&h[(key >> shift) & 255], 1);
+    });
     __syncthreads();
-    for (int i = tid; i < nb; i += kTopThreads) {
-      const uint32_t key = order_key(__ldg(row + i));
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1);
+    // lane l: digits 8 l .. 8 l + 7; above = keys in larger digits
+    int cnt[8], sum = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      cnt[u] = h[8 * lane + u];
+      sum += cnt[u];
     }
-    __syncthreads();
-    if (tid == 0) {
-      int left = need, d = 255;
-      while (d > 0 && hist[d] < left) left -= hist[d--];
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_need = left;
+    int above = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_down_sync(0xffffffffu, above, o);
+      if (lane + o < 32) above += y;
     }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
+    above -= sum;
+    int digit = -1, left = 0, have = 0;
+#pragma unroll
+    for (int u = 7; u >= 0; --u) {
+      if (digit < 0 && above < need && above + cnt[u] >= need) {
+        digit = 8 * lane + u;
+        left = need - above;
+        have = cnt[u];
+      }
+      above += cnt[u];
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, digit >= 0);
+    const int src = __ffs(who) - 1;
+    digit = __shfl_sync(0xffffffffu, digit, src);
+    need = __shfl_sync(0xffffffffu, left, src);
+    have = __shfl_sync(0xffffffffu, have, src);
+    prefix |= (uint32_t)digit << shift;
+    if (have == need) {   // every key of this digit: the threshold is the digit's smallest key
+      need = INT32_MAX;
+      break;
+    }
   }
-  int out = 0, ties = 0;   // taken, and equal to the threshold, before this step
-  for (int i0 = 0; i0 < nb; i0 += kTopThreads) {
-    const int i = i0 + tid;
-    const uint32_t key = i < nb ? order_key(__ldg(row + i)) : 0u;
-    const bool above = i < nb && key > prefix, tie = i < nb && key == prefix;
-    const unsigned tmask = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) warp_tie[warp] = __popc(tmask);
-    __syncthreads();
-    int tb = ties, tsum = 0;
-    for (int w = 0; w < kTopThreads / 32; ++w) {
-      tb += w < warp ? warp_tie[w] : 0;
-      tsum += warp_tie[w];
+  // keep every key above the threshold and the first `need` equal to it (after an
+  // early end: every key at or above it)
+  const bool all = need == INT32_MAX;
+  int2 mine = make_int2(0, 0);   // kept for sure, equal to the threshold
+  each([&](int, uint32_t key) {
+    mine.x += all ? key >= prefix : key > prefix;
+    mine.y += !all && key == prefix;
+  });
+  int2 upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto.x, o), y = __shfl_up_sync(0xffffffffu, upto.y, o);
+    if (lane >= o) {
+      upto.x += x;
+      upto.y += y;
     }
-    const bool keep = above || (tie && tb + __popc(tmask & ((1u << lane) - 1)) < need);
-    const unsigned kmask = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) warp_take[warp] = __popc(kmask);
-    __syncthreads();
-    int ob = out, osum = 0;
-    for (int w = 0; w < kTopThreads / 32; ++w) {
-      ob += w < warp ? warp_take[w] : 0;
-      osum += warp_take[w];
-    }
-    if (keep) dst[ob + __popc(kmask & ((1u << lane) - 1))] = i;
-    out += osum;
-    ties += tsum;
-    __syncthreads();
   }
+  if (lane == 31) part[warp] = upto;
+  __syncthreads();
+  {
+    int2 p = part[lane];   // 32 warps
+    int2 q = p;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, q.x, o), y = __shfl_up_sync(0xffffffffu, q.y, o);
+      if (lane >= o) {
+        q.x += x;
+        q.y += y;
+      }
+    }
+    upto.x += __shfl_sync(0xffffffffu, q.x - p.x, warp);
+    upto.y += __shfl_sync(0xffffffffu, q.y - p.y, warp);
+  }
+  int kept = upto.x - mine.x, ties = upto.y - mine.y;   // before this thread's entries
+  each([&](int i, uint32_t key) {
+    const bool tie = !all && key == prefix, sure = all ? key >= prefix : key > prefix;
+    if (sure || (tie && ties < need)) dst[kept + min(ties, all ? 0 : need)] = i;
+    kept += sure;
+    ties += tie;
+  });
 }
 
 }  // namespace
@@ -274,16 +500,37 @@ cudaError_t launch_block_keys(const sml_cache& index, const int32_t* pages, int 
 
 cudaError_t launch_block_scores(const sml_problem& p, const uint8_t* iq8, const float* iq_scale, const float* iw,
                                 const sml_cache& block, float* scores, int32_t* status, cudaStream_t stream) {
-  const int tiles = (p.max_pages + kScoreBlocks - 1) / kScoreBlocks;
-  return launch_pdl(block_scores_kernel, dim3(p.num_tokens, tiles < 65535 ? tiles : 65535), dim3(kScoreThreads), 0,
-                    stream, 0, batch_of(p, status), iq8, iq_scale, iw, static_cast<const uint8_t*>(block.base),
+  // Tokens per CTA: as many as leave about four CTAs for every SM, which is
+  // what shared memory and TMEM hold, so that a tile's keys are read for as few
+  // CTAs as fill the device.
+  const int tiles = (p.max_pages + kTileBlocks - 1) / kTileBlocks;
+  const long long ctas = 4ll * device_sm_count();
+  long long chunk = ((long long)p.num_tokens * tiles + ctas - 1) / ctas;
+  chunk = chunk < 1 ? 1 : chunk > kChunk ? kChunk : chunk;
+  const int chunks = (int)((p.num_tokens + chunk - 1) / chunk);
+  const auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap qmap;   // the queries as [T * 64 rows][128 B]: one box = the 64 heads of a token
+  const cuuint64_t dims[2] = {SML_INDEX_DIM, (cuuint64_t)p.num_tokens * SML_INDEX_HEADS}, strides[1] = {SML_INDEX_DIM};
+  const cuuint32_t box[2] = {SML_INDEX_DIM, SML_INDEX_HEADS}, one[2] = {1, 1};
+  if (enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(iq8), dims, strides, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const size_t smem = sizeof(ScoreSmem) + 1024;
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(block_scores_kernel), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(block_scores_kernel, dim3(tiles, chunks), dim3(kScoreThreads), smem, stream, 0, qmap,
+                    batch_of(p, status), (int)chunk, iq_scale, iw, static_cast<const uint8_t*>(block.base),
                     (long long)block.num_pages * SML_PAGE_TOKENS, scores);
 }
 
 cudaError_t launch_block_topk(const sml_problem& p, const float* scores, int k, int32_t* blocks, int32_t* blocks_len,
                               int32_t* status, cudaStream_t stream) {
-  return launch_pdl(block_topk_kernel, dim3(p.num_tokens), dim3(kTopThreads), 0, stream, 0, batch_of(p, status), scores,
-                    k, blocks, blocks_len);
+  constexpr int kReg = 16;   // rows of up to 16,384 blocks (a million positions) stay in registers
+  auto kernel = p.max_pages <= kReg * kTopThreads ? block_topk_kernel<kReg> : block_topk_kernel<0>;
+  return launch_pdl(kernel, dim3(p.num_tokens), dim3(kTopThreads), 0, stream, 0, batch_of(p, status), scores, k, blocks,
+                    blocks_len);
 }
 
 }  // namespace sml
