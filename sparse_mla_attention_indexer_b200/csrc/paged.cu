@@ -21,7 +21,13 @@ namespace sml {
 namespace {
 
 constexpr int kKT = 128;                 // keys per tile: two pages
-constexpr int kParts = 4;                // a tile's latent dims arrive and are freed in quarters of 128
+// A tile's latent dims arrive, enter QK^T and PV and are freed in quarters of
+// 128, block part_block(p) as the p-th.  The scales and the RoPE keys come with
+// the second: the products left when the last part lands are then four, and
+// with 32 heads, whose weights for the first two output blocks lie where the
+// RoPE keys were, those are read by then.
+constexpr int kParts = 4, kRopePart = 1;
+__host__ __device__ constexpr int part_block(int part) { return (part + 3) & 3; }
 constexpr int kLatBlock = kKT * 128;     // one 128-B wide block of a tile
 constexpr int kSoftmaxWarps = 16;        // warps 0-15
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
@@ -125,15 +131,17 @@ __device__ __forceinline__ void pages_at(const Params& P, const Tok& tk, int t, 
   if (!vb) b.lg = 0;
 }
 
-// This CTA's range of its head group's tiles, and the token it starts in.
+// This CTA's range [ub, ue) of its head group's tiles, and the token t0 that it
+// starts in (tok0: that token's first tile).
 struct Range {
-  long long total, ub, ue, tok0;   // tok0: first tile of token t0
+  long long total, ub, ue, tok0;
   int used, t0;
 };
 struct PlanSmem {
-  long long part[kThreads / 32];
+  long long part[32];   // per warp of the block
   long long tok0;
   int t0;
+  Tok tok[32];          // the tokens of a batch of at most 32
 };
 
 // a / b of non-negative numbers, in 32 bits where both fit (a 64-bit division
@@ -141,13 +149,46 @@ struct PlanSmem {
 __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
-__device__ __forceinline__ long long range_begin(long long total, int used, int i) { return div_ll(total * i, used); }
 __device__ __forceinline__ int cta_of(long long total, int used, long long u) { return (int)div_ll((u + 1) * used - 1, total); }
 
-template <int kN>
-__device__ Range plan_range(const Params& P, int gi, PlanSmem& S) {
-  const int per = (P.T + kN - 1) / kN, a = min(P.T, (int)threadIdx.x * per), b = min(P.T, a + per);
+// The shares: as few CTAs as give the same longest range.
+__device__ __forceinline__ void share(Range& R, int cpg, int gi) {
+  const long long most = div_ll(R.total + cpg - 1, cpg);
+  R.used = (int)div_ll(R.total + most - 1, most);
+  R.ub = gi < R.used ? div_ll(R.total * gi, R.used) : 0;
+  R.ue = gi < R.used ? div_ll(R.total * (gi + 1), R.used) : 0;
+}
+
+// Token t's lengths: a small batch's are in shared memory, else they are read again.
+__device__ __forceinline__ Tok token_of(const Params& P, const PlanSmem& S, int t) {
+  return P.T <= 32 ? S.tok[t] : token_at(P, t);
+}
+
+// Every thread of the block calls it.  Up to 32 tokens: each warp for itself
+// (with the scan over the block below, 2.0 us instead of 1.0 from the first load
+// to the range).
+__device__ __forceinline__ Range plan_range(const Params& P, int gi, PlanSmem& S) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Range R;
+  if (P.T <= 32) {
+    const Tok tk = token_at(P, min(lane, P.T - 1));
+    if (warp == 0) S.tok[lane] = tk;
+    const int mine = lane < P.T ? tiles_of(tk) : 0;   // at most 2^23 each
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    R.total = __shfl_sync(0xffffffffu, upto, 31);
+    share(R, P.ws.cpg, gi);
+    const unsigned in = __ballot_sync(0xffffffffu, upto - mine <= R.ub && R.ub < upto);
+    R.t0 = __ffs(in) - 1;
+    R.tok0 = __shfl_sync(0xffffffffu, upto - mine, R.t0);
+    __syncthreads();
+    return R;
+  }
+  const int per = (P.T + kThreads - 1) / kThreads, a = min(P.T, (int)threadIdx.x * per), b = min(P.T, a + per);
   long long mine = 0;
   for (int t = a; t < b; ++t) mine += tiles_of(token_at(P, t));
   long long upto = mine;
@@ -158,18 +199,13 @@ __device__ Range plan_range(const Params& P, int gi, PlanSmem& S) {
   }
   if (lane == 31) S.part[warp] = upto;
   __syncthreads();
-  Range R;
   R.total = 0;
   long long before = 0;
-  for (int w = 0; w < kN / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     before += w < warp ? S.part[w] : 0;
     R.total += S.part[w];
   }
-  // as few CTAs as give the same longest range
-  const long long most = div_ll(R.total + P.ws.cpg - 1, P.ws.cpg);
-  R.used = (int)div_ll(R.total + most - 1, most);
-  R.ub = gi < R.used ? range_begin(R.total, R.used, gi) : 0;
-  R.ue = gi < R.used ? range_begin(R.total, R.used, gi + 1) : 0;
+  share(R, P.ws.cpg, gi);
   const long long first = before + upto - mine;   // first tile of token a
   if (first <= R.ub && R.ub < first + mine) {
     long long at = first;
@@ -214,10 +250,17 @@ template <int kFmt, int kHU>
 struct __align__(1024) Smem {
   using F = Fmt<kFmt>;
   static constexpr int kSetBytes = kKT * 2 * kHU * (F::kBf ? 2 : 1);   // both terms of one weight set
-  // With 32 heads per unit the last two weight sets of a tile live where its
-  // RoPE keys were: those are dead once the tile's logits are done.
+  // With 32 heads per unit the weight sets of a tile's first two output blocks
+  // live where its RoPE keys were: those are dead once the tile's logits are done.
   static constexpr bool kOverlay = F::kDs && kHU == 32;
   static constexpr int kOwnSets = kOverlay ? 2 : F::kSets;
+  __device__ __forceinline__ uint32_t set_addr(int b, int buf) const {
+    if (F::kSets == 1) return ptx::smem_u32(pb[0]);
+    if (!kOverlay) return ptx::smem_u32(pb[b]);
+    return b == part_block(0)   ? ptx::smem_u32(pe[buf])
+           : b == part_block(1) ? ptx::smem_u32(pe[buf]) + kSetBytes
+                                : ptx::smem_u32(pb[b == part_block(2) ? 0 : 1]);
+  }
   uint8_t lat[F::kBufs][F::kBlocks][kLatBlock];   // [buffer][block][128 keys x 128 B], SW128
   uint8_t pe[F::kBufs][kKT * 128];                // [buffer][128 keys x 128 B] RoPE keys, SW128
   uint8_t q8[1024 * kHU];   // E4M3: [block] 2 kHU rows (high, then low term) x 128 B, SW128; bf16: 8 blocks of kHU rows
@@ -248,10 +291,10 @@ struct Walk {
   long long u, ue;
   int t, j0;
 };
-__device__ __forceinline__ bool walk_next(const Params& P, Walk& w, int slot, int heads, Seg& s) {
+__device__ __forceinline__ bool walk_next(const Params& P, const PlanSmem& ts, Walk& w, int slot, int heads, Seg& s) {
   if (w.u >= w.ue) return false;
   s.t = w.t;
-  s.tk = token_at(P, w.t);
+  s.tk = token_of(P, ts, w.t);
   const int nt = tiles_of(s.tk), nj = (int)min((long long)(nt - w.j0), w.ue - w.u);
   s.j0 = w.j0;
   s.ne = s.tk.np > 0 ? nj : 0;
@@ -270,11 +313,11 @@ struct Cur {
   int ne, jj, seg, k;
   bool valid;
 };
-__device__ __forceinline__ void cur_seek(Cur& c, const Params& P) {
+__device__ __forceinline__ void cur_seek(Cur& c, const Params& P, const PlanSmem& ts) {
   Seg s;
   c.jj = 0;
   c.valid = false;
-  while (walk_next(P, c.w, 0, 0, s)) {
+  while (walk_next(P, ts, c.w, 0, 0, s)) {
     c.ne = s.ne;
     if (s.ne > 0) {
       c.valid = true;
@@ -282,11 +325,11 @@ __device__ __forceinline__ void cur_seek(Cur& c, const Params& P) {
     }
   }
 }
-__device__ __forceinline__ void cur_next(Cur& c, const Params& P) {
+__device__ __forceinline__ void cur_next(Cur& c, const Params& P, const PlanSmem& ts) {
   ++c.k;
   if (++c.jj < c.ne) return;
   ++c.seg;
-  cur_seek(c, P);
+  cur_seek(c, P, ts);
 }
 
 // Byte address of (row, 16-B chunk) in a 128-B-swizzled tile of 128-B rows.
@@ -497,15 +540,16 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   volatile int* abort = &S.abort;
   const uint32_t T0 = S.tmem_base;
-  const Range R = plan_range<kThreads>(P, gi, S.plan);
+  const PlanSmem& ts = S.plan;
+  const Range R = plan_range(P, gi, S.plan);
   const int slot = (g * P.ws.cpg + gi) * 2;
-  if (warp == kWarpPv && lane == 0) {
+  if (warp == kWarpPv) {
     // the token that this CTA continues, and the CTAs that hold it
     int4 rec = make_int4(-1, 0, 0, 0);
     if (gi < R.used && R.ub > R.tok0)
       rec = make_int4(R.t0, cta_of(R.total, R.used, R.tok0),
-                      cta_of(R.total, R.used, R.tok0 + tiles_of(token_at(P, R.t0)) - 1), gi);
-    P.ws.join[g * P.ws.cpg + gi] = rec;
+                      cta_of(R.total, R.used, R.tok0 + tiles_of(token_of(P, ts, R.t0)) - 1), gi);
+    if (lane == 0) P.ws.join[g * P.ws.cpg + gi] = rec;
   }
   const Walk begin = {R.ub, R.ue, R.t0, (int)(R.ub - R.tok0)};
 
@@ -518,8 +562,8 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     const bool rope = P.rope_dim != 0;
     constexpr int kPartBlocks = F::kBlocks / kParts;
     constexpr uint32_t kPartBytes = kPartBlocks * SML_PAGE_TOKENS * 128;   // of one page
-    const uint32_t last_bytes = kPartBytes + (F::kDs ? SML_PAGE_TOKENS * 16 : 0) + (rope ? SML_PAGE_TOKENS * 128 : 0);
-    while (ok && walk_next(P, w, slot, kHU, s)) {
+    const uint32_t rope_bytes = kPartBytes + (F::kDs ? SML_PAGE_TOKENS * 16 : 0) + (rope ? SML_PAGE_TOKENS * 128 : 0);
+    while (ok && walk_next(P, ts, w, slot, kHU, s)) {
       if (lane == 0 && g == 0) {
         if (!s.tk.ok) raise_fault(P.status, SML_FAULT_LENGTHS);
         if (s.tk.len_bad) raise_fault(P.status, SML_FAULT_TOPK_LEN);
@@ -544,15 +588,13 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           if (ph >= 0) ptx::bulk_prefetch_l2(P.latent + (size_t)ph * F::kPageBytes, F::kPageBytes);
         }
         const uint32_t pages = (p0 >= 0) + (p1 >= 0);
-        // The last part brings the scales and the RoPE keys: with 32 heads the
-        // RoPE keys' place holds the weights of the last two parts until then.
         for (int part = 0; part < kParts; ++part) {
           begun = part;
           if (k >= kBufs) ok = warp_wait(&S.lat_free[buf][part], ((k / kBufs) - 1) & 1, abort);
           if (!ok) break;
           if (lane == 0) {
-            const bool last = part == kParts - 1;
-            if (last) {
+            const bool with_rope = part == kRopePart;
+            if (with_rope) {
               int4 r;   // valid rows of each page: none of one that is not loaded
               r.x = max(0, s.tk.lo - l0 * SML_PAGE_TOKENS);
               r.y = p0 >= 0 ? min(SML_PAGE_TOKENS, s.tk.n - l0 * SML_PAGE_TOKENS) : 0;
@@ -561,17 +603,18 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
               S.rows[k & 3] = r;   // last read by the softmax of tile k - 4
             }
             uint64_t* bar = &S.full[buf][part];
-            ptx::mbar_arrive_expect_tx(bar, pages * (last ? last_bytes : kPartBytes));
+            ptx::mbar_arrive_expect_tx(bar, pages * (with_rope ? rope_bytes : kPartBytes));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const int ph = half ? p1 : p0, y = ph * SML_PAGE_TOKENS, off = half * SML_PAGE_TOKENS * 128;
               if (ph < 0) continue;
 #pragma unroll
               for (int b = 0; b < kPartBlocks; ++b)
-                ptx::tma_load_2d(S.lat[buf][part * kPartBlocks + b] + off, &row_map, bar, 128 * (part * kPartBlocks + b), y);
-              if (last && F::kDs)
+                ptx::tma_load_2d(S.lat[buf][part_block(part) * kPartBlocks + b] + off, &row_map, bar,
+                                 128 * (part_block(part) * kPartBlocks + b), y);
+              if (with_rope && F::kDs)
                 ptx::tma_load_2d(&S.sc[F::kDs ? buf : 0][half * SML_PAGE_TOKENS][0], &scale_map, bar, SML_LATENT_DIM, y);
-              if (last && rope) ptx::tma_load_2d(S.pe[buf] + off, &row_map, bar, F::kPeX, y);
+              if (with_rope && rope) ptx::tma_load_2d(S.pe[buf] + off, &row_map, bar, F::kPeX, y);
             }
           }
           __syncwarp();
@@ -594,7 +637,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     constexpr uint32_t id_q2 = ptx::idesc_f16(2 * kHU, 0, 0, 0);   // both terms
     constexpr uint32_t id_pe = ptx::idesc_f16(kHU, 1, 0, 0);
     const uint32_t q0 = ptx::smem_u32(S.q8), qp = ptx::smem_u32(S.qpe);
-    // One part of a tile's QK^T: 128 latent dims, and with the last the RoPE dims.
+    // One part of a tile's QK^T: 128 latent dims, and with the second the RoPE dims.
     auto issue_qk = [&](int buf, int part) {
       if constexpr (F::kBf) {
         // S^T = C . Q^T + K_pe . Q_pe^T, 16 dims per step
@@ -602,24 +645,24 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         for (int bb = 0; bb < 2; ++bb)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const int b = 2 * part + bb;
+            const int b = 2 * part_block(part) + bb;
             ptx::mma_bf(T0, ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
                         ptx::sdesc_sw128(q0 + b * (kHU * 128) + 32 * kk), id_q1, (part | bb | kk) != 0);
           }
       } else {
         // S_b^T = C_b . [Qhi_b; Qlo_b]^T, 32 dims per step (plain E4M3: one sum over the blocks)
-        const bool split = F::split_terms(kHU, part);
+        const int b = part_block(part);
+        const bool split = F::split_terms(kHU, b);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
           for (int term = 0; term < (split ? 1 : 2); ++term)
-            ptx::mma_f8(T0 + F::col_block(kHU, part), ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][part]) + 32 * kk),
-                        ptx::sdesc_sw128(q0 + (2 * part + term) * (kHU * 128) + 32 * kk), split ? id_q2 : id_q1,
+            ptx::mma_f8(T0 + F::col_block(kHU, b), ptx::sdesc_sw128(ptx::smem_u32(S.lat[buf][b]) + 32 * kk),
+                        ptx::sdesc_sw128(q0 + (2 * b + term) * (kHU * 128) + 32 * kk), split ? id_q2 : id_q1,
                         F::kDs ? (kk | term) != 0 : (part | kk) != 0);
       }
-      if (part < kParts - 1) return;
       const uint32_t pe0 = ptx::smem_u32(S.pe[buf]);
-      if (P.rope_dim) {
+      if (part == kRopePart && P.rope_dim) {
         if constexpr (F::kPlain) {
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
@@ -631,16 +674,16 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
                         id_pe, F::kBf || kk > 0);
         }
       }
-      ptx::mma_commit(&S.s_full);
+      if (part == kParts - 1) ptx::mma_commit(&S.s_full);
     };
     // One elected lane issues, from code with the buffer and part known at
     // compile time, so that the descriptors are constants off a uniform base.
     Cur c;
     c.w = begin;
     c.seg = c.k = 0;
-    cur_seek(c, P);
+    cur_seek(c, P, ts);
     bool ok = true;
-    for (; c.valid; cur_next(c, P)) {
+    for (; c.valid; cur_next(c, P, ts)) {
       const int buf = c.k % kBufs;
       if (c.jj == 0) ok = warp_wait(&S.q_ready, c.seg & 1, abort);                    // the piece's query is staged
       if (ok && c.k > 0) ok = warp_wait(&S.s_free, (c.k - 1) & 1, abort);             // the last tile's S has been read
@@ -675,10 +718,9 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     constexpr uint32_t kGroup = 2 * kHU * (F::kBf ? 2 : 1) * 8;   // bytes of an 8-key group of a weight set
     auto issue_pv = [&](int buf, bool first) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint32_t set = F::kSets == 1 ? ptx::smem_u32(S.pb[0])
-                             : Sm::kOverlay && b >= 2 ? ptx::smem_u32(S.pe[buf]) + (b - 2) * Sm::kSetBytes
-                                                      : ptx::smem_u32(S.pb[Sm::kOverlay ? b & 1 : b]);
+      for (int part = 0; part < kParts; ++part) {
+        const int b = part_block(part);
+        const uint32_t set = S.set_addr(b, buf);
 #pragma unroll
         for (int st = 0; st < kKT / kKeysPerStep; ++st) {
           const uint64_t bd = ptx::sdesc(set + st * (kKeysPerStep / 8) * kGroup, kGroup, 128, 0);
@@ -688,17 +730,16 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           else
             ptx::mma_f8(d, ptx::sdesc(ptx::smem_u32(S.lat[buf][b]) + 4096 * st, 16384, 1024, 2), bd, id_pv, st > 0 || !first);
         }
-        if (b < 3) ptx::mma_commit(&S.lat_free[buf][b]);
+        ptx::mma_commit(&S.lat_free[buf][part]);
       }
       ptx::mma_commit(&S.pv_done);
-      ptx::mma_commit(&S.lat_free[buf][3]);
     };
     Cur c;
     c.w = begin;
     c.seg = c.k = 0;
-    cur_seek(c, P);
+    cur_seek(c, P, ts);
     bool ok = true;
-    for (; c.valid; cur_next(c, P)) {
+    for (; c.valid; cur_next(c, P, ts)) {
       const int buf = c.k % kBufs;
       if (c.jj == 0 && c.seg > 0) ok = warp_wait(&S.o_free, (c.seg - 1) & 1, abort);  // the last piece's O has been read
       ok = ok && warp_wait(&S.p_full, c.k & 1, abort);                                // weights written, masked rows zeroed
@@ -734,7 +775,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     Seg s;
     int k = 0;
     bool ok = true, staged = false;
-    while (walk_next(P, w, slot, kHU, s)) {
+    while (walk_next(P, ts, w, slot, kHU, s)) {
       // every softmax thread is done with the last piece: its S.qs and S.xsum
       ok = softmax_all(ok);
       if (!ok) break;
@@ -765,7 +806,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       float ebf[4] = {1.f, 1.f, 1.f, 1.f}, ebi[4] = {1.f, 1.f, 1.f, 1.f};
       for (int jj = 0; jj < s.ne; ++jj, ++k) {
         const int buf = k % kBufs;
-        ok = ok && warp_wait(&S.full[buf][kParts - 1], (k / kBufs) & 1, abort) && warp_wait(&S.s_full, k & 1, abort);
+        ok = ok && warp_wait(&S.full[buf][kRopePart], (k / kBufs) & 1, abort) && warp_wait(&S.s_full, k & 1, abort);
         ptx::tc_fence_after();
         const int4 rr = S.rows[k & 3];
         const int prow = row & 63;
@@ -941,8 +982,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           const uint32_t off = (row >> 3) * (kHU * 16) + (row & 7) * 16 + ((2 * kHT * hq) >> 4) * 128 + ((2 * kHT * hq) & 15);
 #pragma unroll
           for (int b = 0; b < F::kSets; ++b) {
-            const uint32_t pb = off + (Sm::kOverlay && b >= 2 ? ptx::smem_u32(S.pe[buf]) + (b - 2) * Sm::kSetBytes
-                                                              : ptx::smem_u32(S.pb[Sm::kOverlay ? b & 1 : b]));
+            const uint32_t pb = off + S.set_addr(b, buf);
             const __half2 sc2 = __float2half2_rn(F::kDs ? scv[b] * rk : 1.f);   // at most 1
             uint32_t hi[kHT / 4], lo[kHT / 4];
 #pragma unroll
@@ -978,7 +1018,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       {
         Walk peek = w;
         Seg nx;
-        while (ok && walk_next(P, peek, slot, kHU, nx)) {
+        while (ok && walk_next(P, ts, peek, slot, kHU, nx)) {
           if (nx.ne > 0) {
             stage(nx);
             staged = true;
@@ -1011,15 +1051,16 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           else P.ws.part_lse[s.part + kHT * hq + h] = lse;
         }
       }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {   // (not unrolled: its code is run once a piece, and fetched for it)
         uint32_t ov[2 * kHT];
         tmem_ldn(T0 + kColO + 2 * kHU * b + 2 * kHT * hq + lane_off, ov);
         ptx::tmem_wait_ld(ov);
         const int dim = 128 * b + row;
+        const float eb = b == 0 ? ebi[0] : b == 1 ? ebi[1] : b == 2 ? ebi[2] : ebi[3];
 #pragma unroll
         for (int h = 0; h < kHT; ++h) {
-          const float o = (__uint_as_float(ov[h]) + __uint_as_float(ov[kHT + h])) * osc[h] * ebi[b];
+          const float o = (__uint_as_float(ov[h]) + __uint_as_float(ov[kHT + h])) * osc[h] * eb;
           if (s.whole) {
             const __nv_bfloat16 r = __float2bfloat16_rn(o);
             P.out[(orow + kHT * hq + h) * SML_LATENT_DIM + dim] = *reinterpret_cast<const uint16_t*>(&r);
