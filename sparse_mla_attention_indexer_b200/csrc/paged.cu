@@ -34,6 +34,7 @@ constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kWarpQk = 16, kWarpPv = 17, kWarpLoad = 18;
 constexpr int kThreads = 608;
 constexpr uint32_t kColO = 256;          // TMEM: logits from column 0, O from here
+constexpr float kNoM = -1e30f;            // M_h before a head's first key: any logit is far above it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Weight exponents: a weight is capped at 440 (E4M3's largest value is 448;
@@ -267,9 +268,9 @@ struct __align__(1024) Smem {
   uint8_t qpe[(F::kPlain ? 2 : 1) * kHU * 128];   // RoPE query, SW128 (plain E4M3: high, then low term)
   uint8_t pb[kOwnSets][kSetBytes];                // weight sets: 8-key x 16-B core matrices
   float sc[F::kDs ? F::kBufs : 1][kKT][4];        // [buffer][key] block scales
-  float xmax[4][4][kHU / 4];                      // [head quarter][key quarter][head]
+  __align__(8) float xmax[4][4][kHU / 4];                      // [head quarter][key quarter][head]
   float xscale[4][4][4];                          // [head quarter][key quarter][block]
-  float xsum[4][4][kHU / 4];
+  __align__(8) float xsum[4][4][kHU / 4];
   float qs[kHU];                                  // power-of-two query scale per head
   int4 rows[4];                                   // [tile % 4] valid rows {lo, hi} of each page of the tile
   uint64_t full[F::kBufs][kParts], lat_free[F::kBufs][kParts];   // per quarter of the latent dims
@@ -359,20 +360,17 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float& x0, float& x1) {
   return c;
 }
 // Two weights (at most 448) in half precision as two E4M3 terms, hi + lo: eight
-// significant bits, as many as a bf16 has.  hi is x to 4 significant bits by
-// Veltkamp's splitting (T. J. Dekker, "A floating-point technique for extending
-// the available precision", 1971): c = 129 x rounded, hi = c + (x - c); 129 *
-// 448 fits half precision (the _rn forms: a fused multiply-add would undo the
-// rounding that the splitting rests on).  x - hi is exact.  Below E4M3's smallest normal
-// value 2^-6 each term is off by at most half a subnormal step, 2^-10.
+// significant bits, as many as a bf16 has.  x - hi is exact in half precision.
+// Below E4M3's smallest normal value 2^-6 a term is off by at most half a
+// subnormal step, 2^-10.  (hi without the conversion back, by Veltkamp's
+// splitting in half precision, measured the same.)
 __device__ __forceinline__ uint32_t half2_to_e4m3x2(__half2 x) {
   return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
 }
 __device__ __forceinline__ void split2_e4m3x2(__half2 x, uint32_t& hi, uint32_t& lo) {
-  const __half2 c = __hmul2_rn(x, __float2half2_rn(129.f));
-  const __half2 h = __hadd2_rn(c, __hsub2_rn(x, c));
-  hi = half2_to_e4m3x2(h);
-  lo = half2_to_e4m3x2(__hsub2_rn(x, h));
+  hi = half2_to_e4m3x2(x);
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
+  lo = half2_to_e4m3x2(__hsub2_rn(x, *reinterpret_cast<const __half2*>(&h)));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -793,12 +791,15 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       // logits in log2 units, so that p = 2^(z - M)
       const float zscale = P.sm_scale * (P.ssmax ? P.ssmax_s * logf((float)s.tk.nss) : 1.f) * kLog2e *
                            (F::kPlain ? P.latent_scale : 1.f);
-      float qsh[kHT], M[kHT], lrow[kHT];
+      // Two heads to an instruction (add / fma.f32x2): the scale of their
+      // logits, -M_h and this key row's share of the row sum, in units of 2^M_h.
+      constexpr int kHP = kHT / 2;
+      float2 qz[kHP], nM[kHP], lrow[kHP];
 #pragma unroll
-      for (int h = 0; h < kHT; ++h) {
-        qsh[h] = S.qs[kHT * hq + h];
-        M[h] = -INFINITY;
-        lrow[h] = 0.f;
+      for (int i = 0; i < kHP; ++i) {
+        qz[i] = make_float2(S.qs[kHT * hq + 2 * i] * zscale, S.qs[kHT * hq + 2 * i + 1] * zscale);
+        nM[i] = make_float2(-kNoM, -kNoM);
+        lrow[i] = make_float2(0.f, 0.f);
       }
       // Block scales enter the weights relative to 2^eb, the largest of the
       // block in the piece's first tile, so that blocks of different magnitude
@@ -811,16 +812,47 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         const int4 rr = S.rows[k & 3];
         const int prow = row & 63;
         const bool valid = row < 64 ? prow >= rr.x && prow < rr.y : prow >= rr.z && prow < rr.w;
+        const bool partial = (rr.x | rr.z) != 0 || rr.y != SML_PAGE_TOKENS || rr.w != SML_PAGE_TOKENS;
+        // z = zscale (s_h sum_b scale_b (S_b,hi + S_b,lo) + S_pe) + lk, with lk
+        // the logarithm of the key's largest block scale: 2^(z - M_h) bounds the
+        // key's weights.  Block scales are taken relative to 2^eb, see above.
         float scv[4] = {1.f, 1.f, 1.f, 1.f};
-        float z[kHT];
+        float lk = 0.f, rk = 1.f;   // and rk = 2^-lk
+        float2 z[kHP];
         if constexpr (F::kDs) {
           const float4 f = *reinterpret_cast<const float4*>(S.sc[buf][row]);
-          scv[0] = valid ? f.x : 0.f;
-          scv[1] = valid ? f.y : 0.f;
-          scv[2] = valid ? f.z : 0.f;
-          scv[3] = valid ? f.w : 0.f;
+          scv[0] = f.x;
+          scv[1] = f.y;
+          scv[2] = f.z;
+          scv[3] = f.w;
+          if (partial && !valid) scv[0] = scv[1] = scv[2] = scv[3] = 0.f;
+          if (jj == 0) {
 #pragma unroll
-          for (int h = 0; h < kHT; ++h) z[h] = 0.f;
+            for (int b = 0; b < 4; ++b) {
+              const float x = ptx::warp_max_f32(scv[b]);
+              if (lane == 0) S.xscale[hq][q4][b] = x;
+            }
+            group_sync(hq);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const float x = fmaxf(fmaxf(S.xscale[hq][0][b], S.xscale[hq][1][b]), fmaxf(S.xscale[hq][2][b], S.xscale[hq][3][b]));
+              const int e = min(max((int)((__float_as_uint(x) >> 23) & 255) - 127, -100), 100);
+              ebf[b] = __int_as_float((127 - e) << 23);
+              ebi[b] = __int_as_float((127 + e) << 23);
+            }
+          }
+          const float top = fmaxf(fmaxf(scv[0] * ebf[0], scv[1] * ebf[1]), fmaxf(scv[2] * ebf[2], scv[3] * ebf[3]));
+          lk = lg2(fmaxf(top, 0x1p-60f));
+          rk = ex2(-lk);
+          float2 acc[kHP];
+#pragma unroll
+          for (int i = 0; i < kHP; ++i) acc[i] = make_float2(0.f, 0.f);
+          auto add = [&](const uint32_t* v, float sc) {   // acc += sc v, kHT values
+            const float2 s2 = make_float2(sc, sc);
+#pragma unroll
+            for (int i = 0; i < kHP; ++i)
+              acc[i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[i]);
+          };
 #pragma unroll
           for (int b = 0; b < 4; b += 2) {   // two blocks at a time: their loads overlap
             uint32_t v[2][2 * kHT], w[kHT];
@@ -831,73 +863,61 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
             ptx::reg_fence(v[0]);
             if (F::split_terms(kHU, b + 1)) ptx::reg_fence(v[1]);
             else ptx::reg_fence(w);
-#pragma unroll
-            for (int h = 0; h < kHT; ++h) {
-              z[h] = fmaf(scv[b], __uint_as_float(v[0][h]) + __uint_as_float(v[0][kHT + h]), z[h]);
-              z[h] = fmaf(scv[b + 1],
-                          F::split_terms(kHU, b + 1) ? __uint_as_float(v[1][h]) + __uint_as_float(v[1][kHT + h])
-                                                     : __uint_as_float(w[h]),
-                          z[h]);
+            add(v[0], scv[b]);
+            add(v[0] + kHT, scv[b]);
+            if (F::split_terms(kHU, b + 1)) {
+              add(v[1], scv[b + 1]);
+              add(v[1] + kHT, scv[b + 1]);
+            } else {
+              add(w, scv[b + 1]);
             }
           }
-#pragma unroll
-          for (int h = 0; h < kHT; ++h) z[h] *= qsh[h];
+          const float2 lk2 = make_float2(lk, lk), zs2 = make_float2(zscale, zscale);
           if (P.rope_dim) {
             uint32_t v[kHT];
             tmem_ldn(T0 + F::col_rope(kHU) + kHT * hq + lane_off, v);
             ptx::tmem_wait_ld(v);
 #pragma unroll
-            for (int h = 0; h < kHT; ++h) z[h] += __uint_as_float(v[h]);
+            for (int i = 0; i < kHP; ++i)
+              z[i] = __ffma2_rn(acc[i], qz[i],
+                                __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), zs2, lk2));
+          } else {
+#pragma unroll
+            for (int i = 0; i < kHP; ++i) z[i] = __ffma2_rn(acc[i], qz[i], lk2);
           }
         } else {
           uint32_t v[F::kBf ? kHT : 2 * kHT];
           tmem_ldn(T0 + (F::kBf ? kHT : 2 * kHT) * hq + lane_off, v);
           ptx::tmem_wait_ld(v);
 #pragma unroll
-          for (int h = 0; h < kHT; ++h)
-            z[h] = (__uint_as_float(v[h]) + (F::kBf ? 0.f : __uint_as_float(v[F::kBf ? h : kHT + h]))) * qsh[h];
+          for (int i = 0; i < kHP; ++i) {
+            float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            if constexpr (!F::kBf)
+              x = __fadd2_rn(x, make_float2(__uint_as_float(v[kHT + 2 * i]), __uint_as_float(v[kHT + 2 * i + 1])));
+            z[i] = __fmul2_rn(x, qz[i]);
+          }
         }
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&S.s_free);   // S read: the next tile's QK^T may overwrite it
+        if (partial && !valid) {
 #pragma unroll
-        for (int h = 0; h < kHT; ++h) z[h] = valid ? z[h] * zscale : -INFINITY;
-        if (F::kDs && jj == 0) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float x = ptx::warp_max_f32(scv[b]);
-            if (lane == 0) S.xscale[hq][q4][b] = x;
-          }
-          group_sync(hq);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float x = fmaxf(fmaxf(S.xscale[hq][0][b], S.xscale[hq][1][b]), fmaxf(S.xscale[hq][2][b], S.xscale[hq][3][b]));
-            const int e = min(max((int)((__float_as_uint(x) >> 23) & 255) - 127, -100), 100);
-            ebf[b] = __int_as_float((127 - e) << 23);
-            ebi[b] = __int_as_float((127 + e) << 23);
-          }
+          for (int i = 0; i < kHP; ++i) z[i] = make_float2(-INFINITY, -INFINITY);
         }
-        // This key's weights 2^(z - M_h) scale_b must stay within E4M3's 448:
-        // with lk the logarithm of its largest scale, z + lk - M_h bounds
-        // them.  A bound above the cap, or a head without M_h yet, sends the
-        // quarter's four warps through the exact update (a vote: rare after
-        // the first tile).  bf16: no scales; M_h only keeps 2^(z - M_h) within
-        // 2^16.
-        float lk = 0.f, rk = 1.f;   // and rk = 2^-lk
-        if constexpr (F::kDs) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) scv[b] *= ebf[b];
-          lk = lg2(fmaxf(fmaxf(fmaxf(scv[0], scv[1]), fmaxf(scv[2], scv[3])), 0x1p-60f));
-          rk = ex2(-lk);
-#pragma unroll
-          for (int h = 0; h < kHT; ++h) z[h] += lk;
-        }
+        // The weights 2^(z - M_h) must stay within E4M3's 448.  One above the
+        // cap, or a head without M_h yet, sends the quarter's four warps through
+        // the exact update (a vote: rare after the first tile).  bf16: M_h only
+        // keeps 2^(z - M_h) within 2^16.
         constexpr float kCap = F::kBf ? 16.f : kLog2Cap, kHead = F::kBf ? 0.f : kLog2Head;
-        bool need = false;
+        float2 d[kHP];
+        float most = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < kHT; ++h) need = need || (z[h] != -INFINITY && !(z[h] - M[h] <= kCap));
-        need = group_any(hq, need || !ok);
-        float f[kHT];
+        for (int i = 0; i < kHP; ++i) {
+          d[i] = __fadd2_rn(z[i], nM[i]);
+          most = fmaxf(most, fmaxf(d[i].x, d[i].y));
+        }
+        bool need = group_any(hq, most > kCap || !ok);
+        float2 f[kHP];
         bool any = false;
         if (need) {
           ok = !group_any(hq, !ok);   // a wait that gave up ends the quarter's warps together
@@ -907,25 +927,34 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           // tiles, and the dominant weights keep all eight bits.  O and the
           // row sums scale by 2^(M_old - M_new), exactly.
 #pragma unroll
-          for (int h = 0; h < kHT; ++h) {
-            const float x = ptx::warp_max_f32(z[h]);
-            if (lane == 0) S.xmax[hq][q4][h] = x;
+          for (int i = 0; i < kHP; ++i) {
+            const float x = ptx::warp_max_f32(z[i].x), y = ptx::warp_max_f32(z[i].y);
+            if (lane == 0) *reinterpret_cast<float2*>(&S.xmax[hq][q4][2 * i]) = make_float2(x, y);
           }
           group_sync(hq);
-#pragma unroll
-          for (int h = 0; h < kHT; ++h) {
-            const float e = fmaxf(fmaxf(S.xmax[hq][0][h], S.xmax[hq][1][h]), fmaxf(S.xmax[hq][2][h], S.xmax[hq][3][h]));
-            f[h] = 1.f;
-            if (e != -INFINITY && !(e - M[h] <= kCap)) {
-              const float Mn = ceilf(e - kHead);
-              if (M[h] != -INFINITY) {
-                const float d = M[h] - Mn;   // a negative integer
-                f[h] = d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23);
-                lrow[h] *= f[h];
-                any = true;
-              }
-              M[h] = Mn;
+          auto raise = [&](float e, float& neg, float& fac) {   // e: the tile's largest z of a head
+            fac = 1.f;
+            if (!(e + neg > kCap)) return;
+            const float Mn = ceilf(e - kHead);
+            if (neg != -kNoM) {
+              const float by = -neg - Mn;   // a negative integer
+              fac = by < -126.f ? 0.f : __int_as_float((127 + (int)by) << 23);
+              any = true;
             }
+            neg = -Mn;
+          };
+#pragma unroll
+          for (int i = 0; i < kHP; ++i) {
+            float2 e = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int qq = 0; qq < 4; ++qq) {
+              const float2 x = *reinterpret_cast<const float2*>(&S.xmax[hq][qq][2 * i]);
+              e = make_float2(fmaxf(e.x, x.x), fmaxf(e.y, x.y));
+            }
+            raise(e.x, nM[i].x, f[i].x);
+            raise(e.y, nM[i].y, f[i].y);
+            lrow[i] = __fmul2_rn(lrow[i], f[i]);
+            d[i] = __fadd2_rn(z[i], nM[i]);
           }
         }
         // The last tile's PV reads the weights and accumulates into O: it is
@@ -945,17 +974,17 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
               tmem_ldn(a, ov);
               ptx::tmem_wait_ld(ov);
 #pragma unroll
-              for (int h = 0; h < 2 * kHT; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * f[h % kHT]);
+              for (int h = 0; h < 2 * kHT; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * (h & 1 ? f[h % kHT / 2].y : f[h % kHT / 2].x));
               tmem_stn(a, ov);
             }
             ptx::tmem_wait_st();
           }
         }
+        // p: the weights times this key's largest scale
 #pragma unroll
-        for (int h = 0; h < kHT; ++h) {
-          const float p = z[h] == -INFINITY ? 0.f : ex2(z[h] - M[h]);   // times this key's largest scale
-          lrow[h] = fmaf(p, rk, lrow[h]);
-          z[h] = p;
+        for (int i = 0; i < kHP; ++i) {
+          d[i] = make_float2(ex2(d[i].x), ex2(d[i].y));
+          lrow[i] = __ffma2_rn(d[i], make_float2(rk, rk), lrow[i]);
         }
         // weights: keys by [high | low] terms of each head quarter
         if constexpr (F::kBf) {
@@ -963,9 +992,9 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           uint32_t hi[kHT / 2], lo[kHT / 2];
 #pragma unroll
           for (int i = 0; i < kHT / 2; ++i) {
-            const __nv_bfloat162 hv = __floats2bfloat162_rn(z[2 * i], z[2 * i + 1]);
+            const __nv_bfloat162 hv = __floats2bfloat162_rn(d[i].x, d[i].y);
             const float2 hf = __bfloat1622float2(hv);
-            const __nv_bfloat162 lv = __floats2bfloat162_rn(z[2 * i] - hf.x, z[2 * i + 1] - hf.y);
+            const __nv_bfloat162 lv = __floats2bfloat162_rn(d[i].x - hf.x, d[i].y - hf.y);
             hi[i] = *reinterpret_cast<const uint32_t*>(&hv);
             lo[i] = *reinterpret_cast<const uint32_t*>(&lv);
           }
@@ -976,14 +1005,14 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
             st_v4(pb + 128, lo[0], lo[1], lo[2], lo[3]);
           }
         } else {
-          __half2 p2[kHT / 2];
+          __half2 p2[kHP];
 #pragma unroll
-          for (int i = 0; i < kHT / 2; ++i) p2[i] = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
+          for (int i = 0; i < kHP; ++i) p2[i] = __floats2half2_rn(d[i].x, d[i].y);
           const uint32_t off = (row >> 3) * (kHU * 16) + (row & 7) * 16 + ((2 * kHT * hq) >> 4) * 128 + ((2 * kHT * hq) & 15);
 #pragma unroll
           for (int b = 0; b < F::kSets; ++b) {
             const uint32_t pb = off + S.set_addr(b, buf);
-            const __half2 sc2 = __float2half2_rn(F::kDs ? scv[b] * rk : 1.f);   // at most 1
+            const __half2 sc2 = __float2half2_rn(F::kDs ? scv[b] * ebf[b] * rk : 1.f);   // at most 1
             uint32_t hi[kHT / 4], lo[kHT / 4];
 #pragma unroll
             for (int i = 0; i < kHT / 4; ++i) {
@@ -1000,7 +1029,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         // A masked row may hold anything, and 0 x NaN is NaN in the product:
         // it is zeroed (QK^T, done with this tile, only ever spoiled that
         // row's own logits).
-        if (!valid) {
+        if (partial && !valid) {
 #pragma unroll
           for (int b = hq; b < F::kBlocks; b += 4) {
             const uint32_t a = ptx::smem_u32(S.lat[buf][b]) + (row >> 3) * 1024 + (row & 7) * 128;
@@ -1033,11 +1062,14 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       if (!ok) break;
       ptx::tc_fence_after();
 #pragma unroll
-      for (int h = 0; h < kHT; ++h) {
-        float v = lrow[h];
+      for (int i = 0; i < kHP; ++i) {
+        float2 v = lrow[i];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) S.xsum[hq][q4][h] = v;
+        for (int o = 16; o > 0; o >>= 1) {
+          v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+          v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+        if (lane == 0) *reinterpret_cast<float2*>(&S.xsum[hq][q4][2 * i]) = v;
       }
       group_sync(hq);
       float osc[kHT];
@@ -1046,7 +1078,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         const float l = S.xsum[hq][0][h] + S.xsum[hq][1][h] + S.xsum[hq][2][h] + S.xsum[hq][3][h];
         osc[h] = l > 0.f ? (F::kPlain ? P.latent_scale : 1.f) / l : l == 0.f ? 0.f : l;   // NaN stays
         if (q4 == 0 && lane == 0) {
-          const float lse = l == 0.f ? -INFINITY : (M[h] + log2f(l)) * kLn2;
+          const float lse = l == 0.f ? -INFINITY : (log2f(l) - (h & 1 ? nM[h / 2].y : nM[h / 2].x)) * kLn2;
           if (s.whole) P.lse[orow + kHT * hq + h] = lse;
           else P.ws.part_lse[s.part + kHT * hq + h] = lse;
         }
