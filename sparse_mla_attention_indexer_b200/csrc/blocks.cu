@@ -344,8 +344,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// One CTA per token; thread i owns the row's entries [i c, i c + c), so that one
-// scan over the threads gives every kept entry its place in ascending order.
+// One CTA per token; warp w owns the row's entries [32 c w, 32 c (w + 1)), c
+// steps of one entry a lane, so that loads are coalesced and a scan over the
+// warps and a ballot a step give every kept entry its place in ascending order.
 // The threshold is the k-th largest key, by up to four rounds of an 8-bit
 // histogram that every warp scans for itself; a round whose digit holds exactly
 // the keys still wanted is the last.  kReg > 0: rows of up to kReg entries a
@@ -380,21 +381,28 @@ block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __r
     return;
   }
   if (take == 0) return;
-  const int c = (nb + kTopThreads - 1) / kTopThreads, i0 = min(nb, tid * c), i1 = min(nb, i0 + c);
+  const int c = (nb + kTopThreads - 1) / kTopThreads, i0 = warp * c * 32 + lane;
   uint32_t reg[kReg > 0 ? kReg : 1];
   if constexpr (kReg > 0) {
 #pragma unroll
-    for (int u = 0; u < kReg; ++u)
-      if (u < c) reg[u] = i0 + u < i1 ? order_key(__ldg(row + i0 + u)) : 0u;
+    for (int u = 0; u < kReg; ++u) {
+      if (u >= c) break;
+      reg[u] = i0 + 32 * u < nb ? order_key(__ldg(row + i0 + 32 * u)) : 0u;
+    }
   }
-  // f(index, key) for every entry of this thread, in order
+  // f(index, key, whether there is one) for every step, by whole warps
   auto each = [&](auto&& f) {
     if constexpr (kReg > 0) {
 #pragma unroll
-      for (int u = 0; u < kReg; ++u)
-        if (u < c && i0 + u < i1) f(i0 + u, reg[u]);
+      for (int u = 0; u < kReg; ++u) {
+        if (u >= c) break;
+        f(i0 + 32 * u, reg[u], i0 + 32 * u < nb);
+      }
     } else {
-      for (int i = i0; i < i1; ++i) f(i, order_key(__ldg(row + i)));
+      for (int u = 0; u < c; ++u) {
+        const int i = i0 + 32 * u;
+        f(i, i < nb ? order_key(__ldg(row + i)) : 0u, i < nb);
+      }
     }
   };
   static_assert(kTopThreads == 4 * 256, "a thread clears one counter");
@@ -406,7 +414,8 @@ block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __r
   for (int round = 0; round < 4; ++round) {
     const int shift = 24 - 8 * round;
     int* h = hist[round];
-    each([&](int, uint32_t key) {
+    each([&](int, uint32_t key, bool there) {
+      if (!there) return;
       if (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&h[(key >> shift) & 255], 1);
     });
     __syncthreads();
@@ -448,12 +457,19 @@ block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __r
   // keep every key above the threshold and the first `need` equal to it (after an
   // early end: every key at or above it)
   const bool all = need == INT32_MAX;
-  int2 mine = make_int2(0, 0);   // kept for sure, equal to the threshold
-  each([&](int, uint32_t key) {
-    mine.x += all ? key >= prefix : key > prefix;
-    mine.y += !all && key == prefix;
+  auto sure_of = [&](uint32_t key, bool there) {
+    return __ballot_sync(0xffffffffu, there && (all ? key >= prefix : key > prefix));
+  };
+  auto tie_of = [&](uint32_t key, bool there) { return __ballot_sync(0xffffffffu, there && !all && key == prefix); };
+  int2 mine = make_int2(0, 0);   // this warp's: kept for sure, equal to the threshold
+  each([&](int, uint32_t key, bool there) {
+    mine.x += __popc(sure_of(key, there));
+    mine.y += __popc(tie_of(key, there));
   });
-  int2 upto = mine;
+  if (lane == 0) part[warp] = mine;
+  __syncthreads();
+  const int2 p = part[lane];   // 32 warps
+  int2 upto = p;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, upto.x, o), y = __shfl_up_sync(0xffffffffu, upto.y, o);
@@ -462,28 +478,15 @@ block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __r
       upto.y += y;
     }
   }
-  if (lane == 31) part[warp] = upto;
-  __syncthreads();
-  {
-    int2 p = part[lane];   // 32 warps
-    int2 q = p;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, q.x, o), y = __shfl_up_sync(0xffffffffu, q.y, o);
-      if (lane >= o) {
-        q.x += x;
-        q.y += y;
-      }
-    }
-    upto.x += __shfl_sync(0xffffffffu, q.x - p.x, warp);
-    upto.y += __shfl_sync(0xffffffffu, q.y - p.y, warp);
-  }
-  int kept = upto.x - mine.x, ties = upto.y - mine.y;   // before this thread's entries
-  each([&](int i, uint32_t key) {
-    const bool tie = !all && key == prefix, sure = all ? key >= prefix : key > prefix;
-    if (sure || (tie && ties < need)) dst[kept + min(ties, all ? 0 : need)] = i;
-    kept += sure;
-    ties += tie;
+  int kept = __shfl_sync(0xffffffffu, upto.x - p.x, warp), ties = __shfl_sync(0xffffffffu, upto.y - p.y, warp);
+  const unsigned below = (1u << lane) - 1;
+  each([&](int i, uint32_t key, bool there) {   // kept, ties: before this step's entries
+    const unsigned sure = sure_of(key, there), tie = tie_of(key, there);
+    const int t0 = ties + __popc(tie & below);
+    if ((sure >> lane & 1) || ((tie >> lane & 1) && t0 < need))
+      dst[kept + __popc(sure & below) + (all ? 0 : min(t0, need))] = i;
+    kept += __popc(sure);
+    ties += __popc(tie);
   });
 }
 
