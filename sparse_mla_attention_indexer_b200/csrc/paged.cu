@@ -137,9 +137,11 @@ __device__ __forceinline__ void pages_at(const Params& P, const Tok& tk, int t, 
 struct Range {
   long long total, ub, ue, tok0;
   int used, t0;
+  int m;   // > 0: m CTAs to every token, see share
 };
 struct PlanSmem {
   long long part[32];   // per warp of the block
+  int longest[32];
   long long tok0;
   int t0;
   Tok tok[32];          // the tokens of a batch of at most 32
@@ -152,12 +154,39 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 }
 __device__ __forceinline__ int cta_of(long long total, int used, long long u) { return (int)div_ll((u + 1) * used - 1, total); }
 
-// The shares: as few CTAs as give the same longest range.
-__device__ __forceinline__ void share(Range& R, int cpg, int gi) {
+// Two ways to share the tiles.  (1) Equal contiguous ranges, as few as give the
+// same longest one; a range may hold the ends of two tokens.  (2) m = cpg / T
+// CTAs to every token, each an equal piece of it: no CTA has more than one piece,
+// but the longest token decides.  A piece costs about as much as three tiles
+// more (its query, its first tile, its output), and joining split tokens two.
+// 128 heads (37 CTAs a head group), 32 tokens: over 32 selected blocks, selection
+// included, 63 us with whole tokens and 81 with equal ranges; over 60,000 tokens
+// of context 992 and 940.
+__device__ __forceinline__ void share(Range& R, int T, int cpg, int gi, int longest) {
   const long long most = div_ll(R.total + cpg - 1, cpg);
+  R.m = T <= cpg ? (int)((unsigned)cpg / (unsigned)T) : 0;
+  if (R.m > 0 && (longest + R.m - 1) / R.m + 3 + (R.m > 1 ? 2 : 0) <= most + 8) {
+    R.used = R.m * T;
+    R.t0 = (int)((unsigned)gi / (unsigned)R.m);
+    return;   // the range follows from token t0's tiles, see piece
+  }
+  R.m = 0;
   R.used = (int)div_ll(R.total + most - 1, most);
   R.ub = gi < R.used ? div_ll(R.total * gi, R.used) : 0;
   R.ue = gi < R.used ? div_ll(R.total * (gi + 1), R.used) : 0;
+}
+// Way (2): this CTA's piece of token t0, which has nt tiles (nt < m: some of the
+// m CTAs have none).
+__device__ __forceinline__ void piece(Range& R, int gi, int nt) {
+  const int m = min(R.m, nt), i = gi - R.t0 * R.m;
+  R.tok0 = 0;
+  R.ub = gi < R.used && i < m ? div_ll((long long)nt * i, m) : 0;
+  R.ue = gi < R.used && i < m ? div_ll((long long)nt * (i + 1), m) : 0;
+}
+// The CTAs that hold a token whose first tile is tok0, of nt tiles.
+__device__ __forceinline__ int2 holders(const Range& R, int nt) {
+  if (R.m > 0) return make_int2(R.t0 * R.m, R.t0 * R.m + min(R.m, nt) - 1);
+  return make_int2(cta_of(R.total, R.used, R.tok0), cta_of(R.total, R.used, R.tok0 + nt - 1));
 }
 
 // Token t's lengths: a small batch's are in shared memory, else they are read again.
@@ -182,7 +211,12 @@ __device__ __forceinline__ Range plan_range(const Params& P, int gi, PlanSmem& S
       if (lane >= o) upto += y;
     }
     R.total = __shfl_sync(0xffffffffu, upto, 31);
-    share(R, P.ws.cpg, gi);
+    share(R, P.T, P.ws.cpg, gi, __reduce_max_sync(0xffffffffu, mine));
+    if (R.m > 0) {
+      piece(R, gi, __shfl_sync(0xffffffffu, mine, min(R.t0, P.T - 1)));
+      __syncthreads();
+      return R;
+    }
     const unsigned in = __ballot_sync(0xffffffffu, upto - mine <= R.ub && R.ub < upto);
     R.t0 = __ffs(in) - 1;
     R.tok0 = __shfl_sync(0xffffffffu, upto - mine, R.t0);
@@ -191,22 +225,36 @@ __device__ __forceinline__ Range plan_range(const Params& P, int gi, PlanSmem& S
   }
   const int per = (P.T + kThreads - 1) / kThreads, a = min(P.T, (int)threadIdx.x * per), b = min(P.T, a + per);
   long long mine = 0;
-  for (int t = a; t < b; ++t) mine += tiles_of(token_at(P, t));
+  int longest = 0;
+  for (int t = a; t < b; ++t) {
+    const int nt = tiles_of(token_at(P, t));
+    mine += nt;
+    longest = max(longest, nt);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += y;
   }
-  if (lane == 31) S.part[warp] = upto;
+  if (lane == 31) {
+    S.part[warp] = upto;
+    S.longest[warp] = longest;
+  }
   __syncthreads();
   R.total = 0;
   long long before = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     before += w < warp ? S.part[w] : 0;
     R.total += S.part[w];
+    longest = max(longest, S.longest[w]);
   }
-  share(R, P.ws.cpg, gi);
+  share(R, P.T, P.ws.cpg, gi, longest);
+  if (R.m > 0) {
+    piece(R, gi, tiles_of(token_at(P, min(R.t0, P.T - 1))));
+    return R;
+  }
   const long long first = before + upto - mine;   // first tile of token a
   if (first <= R.ub && R.ub < first + mine) {
     long long at = first;
@@ -544,9 +592,10 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
   if (warp == kWarpPv) {
     // the token that this CTA continues, and the CTAs that hold it
     int4 rec = make_int4(-1, 0, 0, 0);
-    if (gi < R.used && R.ub > R.tok0)
-      rec = make_int4(R.t0, cta_of(R.total, R.used, R.tok0),
-                      cta_of(R.total, R.used, R.tok0 + tiles_of(token_of(P, ts, R.t0)) - 1), gi);
+    if (R.ub > R.tok0 && R.ub < R.ue) {
+      const int2 h = holders(R, tiles_of(token_of(P, ts, R.t0)));
+      rec = make_int4(R.t0, h.x, h.y, gi);
+    }
     if (lane == 0) P.ws.join[g * P.ws.cpg + gi] = rec;
   }
   const Walk begin = {R.ub, R.ue, R.t0, (int)(R.ub - R.tok0)};
