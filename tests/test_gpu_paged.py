@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import blocks as OB, dsa
+from oracle import blocks as OB, dsa, formats as F
 from sparse_mla_attention_indexer_b200 import sml, synth
 from sparse_mla_attention_indexer_b200.device import DeviceWorkload
 from tests import paged_cases as PC
@@ -321,3 +321,116 @@ def test_paged_and_sparse_attention_agree_where_the_selection_is_everything():
     out, lse = run_blocks(wl, all_blocks, count)
     for t in range(wl.T):
         PC.check("blocks", out[t], lse[t], want[t])
+
+
+@pytest.mark.parametrize("spread", [3, 7])
+def test_block_scales_of_different_magnitude(spread):
+    """The four blocks of a row 2^spread apart from their neighbours, and rows scaled by up to
+    2^spread either way.  Besides the bounds above, each term of a weight is off by up to half of
+    E4M3's subnormal step: 2^-9 in all, in units in which the largest p_i sc_ib / 2^eb_b of a key
+    and block is at least 28, 2^eb_b being within a factor 2 below the block's largest scale E_b
+    among the first 128 keys.  An output of block b is then off by at most
+    2^-9 / 28 * max_i,b'(p_i 2 sc_ib' / E_b') * E_b * sum_i |code_ib|."""
+    wl = synth.make_workload(f"paged/spread/{spread}", [300, 1100], [1, 2], 16, layers=(("l", 64, False, None),))
+    rows = wl.latent.reshape(-1, 656)
+    sc = np.ascontiguousarray(rows[:, 512:528]).view("<f4")
+    rng = synth.stream(spread, "paged/spread")
+    row = np.exp2(rng.uniform(-spread, spread, (len(sc), 1)))
+    block = np.exp2(spread * (np.arange(4) - 3.0))
+    with np.errstate(over="ignore", invalid="ignore"):
+        rows[:, 512:528] = (sc * row * block).astype("<f4").view(np.uint8).reshape(-1, 16)
+    out, lse = paged(PC.spoil_unused(wl))
+    n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
+    for t in range(wl.T):
+        o, l, tol, ltol = PC.expect(wl, 0, t, np.arange(int(n_all[t])))
+        r, n = int(dsa.request_of_tokens(wl.cu_q)[t]), int(n_all[t])
+        pages, rw = F.physical(wl.block_table[r], np.arange(n))
+        c, k_pe = F.latent_rows(wl.latent, pages, rw)
+        s4 = np.ascontiguousarray(wl.latent.reshape(-1, 656)[pages * 64 + rw, 512:528]).view("<f4").astype(np.float64)
+        z = wl.sm_scale * (F.decode_bf16(wl.layers[0].q[t]) @ np.concatenate([c, k_pe], 1).T)
+        p = np.exp(z - l[:, None])
+        E = s4[:128].max(0)
+        unit = (p * (2 * s4 / E).max(1)[None]).max(1)                            # [H]
+        codes = np.abs(c.reshape(n, 4, 128) / s4[:, :, None]).sum(0)             # [4, 128]
+        tol = tol + 2.0 ** -9 / 28 * unit[:, None] * (E[:, None] * codes).reshape(1, 512)
+        PC.check(f"spread {spread} token {t}", out[t], lse[t], (o, l, tol, ltol))
+
+
+def test_pages_past_four_gigabytes():
+    """A pool of 4.4 GB whose last pages hold the rows: offsets that do not fit 32 bits."""
+    wl = synth.make_workload("paged/far", [700, 130], [1, 1], 16, layers=(("l", 64, False, None),))
+    far = 105000
+    dw = DeviceWorkload(wl)
+    pool = torch.empty((far + wl.num_pages) * synth.LATENT_PAGE, dtype=torch.uint8, device="cuda")
+    assert far * synth.LATENT_PAGE > 2 ** 32
+    pool[far * synth.LATENT_PAGE:] = dw.latent
+    table = dw.block_table + far
+    p = sml.make_problem(num_heads=16, topk=1, rope_dim=64, cu_q=dw.cu_q, ctx_len=dw.ctx_len, block_table=table,
+                         max_ctx=700, sm_scale=wl.sm_scale, num_tokens=2)
+    out, lse = buffers(2, 16)
+    ws = workspace(p)
+    sml.sml_paged_mla_decode(p, dw.layers[0].q, pool, out, lse, ws)
+    assert sml.sml_read_device_status(ws) == (sml.SML_OK, 0)
+    check_all("far", wl, host(out), host(lse))
+    slot = torch.tensor([far * 64 + 5, (far + 3) * 64 + 63], dtype=torch.int32, device="cuda")
+    c = torch.empty(2, 512, dtype=torch.bfloat16, device="cuda")
+    near = torch.empty_like(c)
+    sml.sml_latent_cache_read(slot, pool, c)
+    sml.sml_latent_cache_read(slot - far * 64, dw.latent, near)
+    assert torch.equal(c.view(torch.int16), near.view(torch.int16))      # an unused row may hold NaN
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own workspace and outputs."""
+    works = [synth.make_workload(f"paged/streams/{i}", lens, qs, 32, layers=(("l", 64, False, None),))
+             for i, (lens, qs) in enumerate((([9000, 130, 64], [1, 2, 1]), ([40000], [3])))]
+    dws = [DeviceWorkload(w) for w in works]
+    ps = [d.problem(0) for d in dws]
+    wss = [workspace(p) for p in ps]
+    bufs = [[buffers(w.T, 32) for _ in range(4)] for w in works]
+    streams = [torch.cuda.Stream() for _ in works]
+    torch.cuda.synchronize()
+    for rep in range(4):
+        for d, p, ws, b, st in zip(dws, ps, wss, bufs, streams):
+            with torch.cuda.stream(st):
+                sml.sml_paged_mla_decode(p, d.layers[0].q, d.latent, *b[rep], ws)
+    torch.cuda.synchronize()
+    for w, ws, b in zip(works, wss, bufs):
+        assert sml.sml_read_device_status(ws) == (sml.SML_OK, 0)
+        check_all("stream", w, host(b[0][0]), host(b[0][1]))
+        for out, lse in b[1:]:
+            assert torch.equal(out, b[0][0]) and torch.equal(lse, b[0][1])
+
+
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 100, 148, 149, 700])
+def test_every_way_to_share_the_tiles(T):
+    """Batches around the borders of the plan: one warp's batch, one CTA a token, more tokens than
+    CTAs; equal lengths (whole tokens) and one long request among short ones (equal ranges)."""
+    for long in (0, 9000):
+        lens = [130 + 64 * (t % 3) for t in range(T)]
+        lens[T // 2] = max(lens[T // 2], long)
+        wl = synth.make_workload(f"paged/share/{T}/{long}", lens, [1] * T, 16, layers=(("l", 64, False, None),))
+        out, lse = paged(wl)
+        check_all(f"T {T} long {long}", wl, out, lse, tokens=sorted({0, T // 2, T - 1, T // 3, max(0, T // 2 - 1)}))
+
+
+def test_one_workspace_for_both_kinds_of_attention():
+    """A workspace large enough for both serves the sparse layer and the paged calls in turn (the
+    top-k counters in it stay zero)."""
+    wl = synth.make_workload("paged/ws", [140000, 900], [1, 2], 16)
+    dw = DeviceWorkload(wl)
+    p, lay = dw.problem(0), dw.layers[0]
+    size = max(sml.sml_workspace_size(p, sml.SML_STAGE_LAYER), sml.sml_workspace_size(p, sml.SML_STAGE_PAGED))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    sml.sml_workspace_init(ws)
+    first = None
+    for _ in range(3):
+        idx, ln, so, sl = dw.outputs()
+        sml.sml_run_layer(p, lay.q, lay.iq8, lay.iq_scale, lay.iw, dw.latent, dw.index_cache, None, None, idx, ln, so, sl, ws)
+        out, lse = buffers(wl.T, 16)
+        sml.sml_paged_mla_decode(p, lay.q, dw.latent, out, lse, ws, window=3000)
+        now = [t.clone() for t in (idx, ln, so, sl, out, lse)]
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(first, now))
+    assert sml.sml_read_device_status(ws) == (sml.SML_OK, 0)
+    check_all("after the sparse layer", wl, host(out), host(lse), window=3000)
