@@ -319,11 +319,15 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
         s[2] = fmaf(wb.z, fmaxf(__uint_as_float(v1[4 * c + 2]), 0.f), s[2]);
         s[3] = fmaf(wb.w, fmaxf(__uint_as_float(v1[4 * c + 3]), 0.f), s[3]);
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&S.acc_free[acc]);   // D and the weights have been read
       if (j < S.nb[i])
         scores[(size_t)(t0 + i) * b.max_pages + j] = there ? ((s[0] + s[1]) + (s[2] + s[3])) * S.fac[i] * sb : NAN;
+      // D and the weights have been read: the arrival lets the next product and
+      // TMA overwrite them.  Loads of the weights that are only issued may still
+      // be on their way; the proxy fence puts them before TMA's writes.
+      ptx::fence_proxy_async();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.acc_free[acc]);
       ++k;
     }
   }

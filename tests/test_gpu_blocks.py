@@ -84,19 +84,19 @@ def run_scores(wl, pool, vis=None):
     return scores.cpu().numpy(), sml.sml_read_device_status(ws)
 
 
-def check_scores(wl, pool, got, n_all):
+def check_scores(wl, pool, got, n_all, tokens=None):
     """Exact FP8 products; 128 of them, then 64 weighted heads, are summed in fp32: at most
     (128 + 64 + 4) roundings of 2^-24 of the summed terms' size, and as much again for the order."""
     v = wl.view(0)
     req = dsa.request_of_tokens(wl.cu_q)
-    q_abs = np.abs(F.decode_e4m3(v.iq8)) * v.iq_scale[:, None, None].astype(np.float64)
-    for t in range(wl.T):
+    for t in range(wl.T) if tokens is None else tokens:
         n = int(n_all[t])
         c = dsa.ssmax_factor(wl.ssmax, wl.ssmax_s_index, n) if n else 0.0
         want, _ = OB.block_scores_row(v.iq8[t], v.iq_scale[t], v.iw[t], pool, wl.block_table[req[t]], n, c)
         pages = wl.block_table[req[t], :OB.candidates(n)].astype(np.int64)
         k_abs = np.abs(F.indexer_keys(pool, pages // 64, pages % 64))
-        size = abs(c) * (np.abs(v.iw[t])[:, None] * (q_abs[t] @ k_abs.T)).sum(0)
+        q_abs = np.abs(F.decode_e4m3(v.iq8[t])) * float(v.iq_scale[t])
+        size = abs(c) * (np.abs(v.iw[t])[:, None] * (q_abs @ k_abs.T)).sum(0)
         d = np.abs(got[t, :len(want)] - want)
         assert (d <= 2 * 196 * 2.0 ** -24 * size).all(), f"token {t}: {d.max():.3e}"
         assert (got[t, len(want):] == 123.0).all(), f"token {t}: entries past the candidates written"
@@ -110,6 +110,25 @@ def test_block_scores(lens, qs, ssmax):
     got, status = run_scores(wl, pool)
     assert status == (sml.SML_OK, 0)
     check_scores(wl, pool, got, dsa.visible_lengths(wl.cu_q, wl.ctx_len))
+
+
+def test_block_scores_of_a_long_chunk_are_the_same_every_time():
+    """A prompt's chunk: CTAs of sixteen tokens, which take their queries and weights through
+    buffers that are filled again while others are read; ten runs, one after the other and
+    overlapping, give the same bits."""
+    wl, pool = scored("bs/chunk", [20000, 700], [2900, 100], ssmax=True)
+    dw = DeviceWorkload(wl)
+    p, lay, ws, d_pool = dw.problem(0), dw.layers[0], status_ws(), dev(pool)
+    runs = [torch.full((wl.T, wl.max_pages), 123.0, device="cuda") for _ in range(10)]
+    for i, scores in enumerate(runs):
+        sml.sml_block_scores(p, lay.iq8, lay.iq_scale, lay.iw, d_pool, scores, ws)
+        if i < 4:
+            torch.cuda.synchronize()
+    assert sml.sml_read_device_status(ws) == (sml.SML_OK, 0)
+    for scores in runs[1:]:
+        assert torch.equal(scores, runs[0])
+    n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
+    check_scores(wl, pool, runs[0].cpu().numpy(), n_all, tokens=list(range(0, wl.T, 41)) + list(range(2880, 2920)))
 
 
 def test_block_scores_given_lengths_and_bad_pages():
