@@ -8,7 +8,41 @@
 //   z_i = sm_scale * c_t * (q_nope . c_hat_i + q_pe . k_pe_i)
 //   out = sum_i softmax(z)_i c_hat_i,   lse = ln sum_i exp(z_i)
 // over the positions i that the token attends to, in one pass over the rows
-// with a running maximum and sum per head.
+// with a running exponent and sum per head.
+//
+// A unit is (query token, group of 16 heads, or 32 of 32 heads and more, tile of
+// two pages = 128 keys).  One CTA per SM works out its range of them from the
+// device's lengths (plan_range) and walks it:
+//   * warp 18 looks up pages and loads them by TMA, 64 rows x 128 B a box in the
+//     128-B swizzle, into two tile buffers (one of bf16), a quarter of the
+//     latent dims at a time;
+//   * warp 16 issues S^T = C Q^T (keys as M, heads as N: 16 or 32 heads as M
+//     would waste half of the smallest M and more), straight from the E4M3 codes,
+//     the bf16 query split exactly into two E4M3 terms; one accumulator per block
+//     scale, RoPE apart in bf16;
+//   * warps 0-15 read S^T (thread = key x a quarter of the heads), scale, take
+//     2^(z - M_h) and write the weights, block scale folded in, as two E4M3
+//     terms (bf16 pools: two bf16 terms);
+//   * warp 17 issues O^T += C^T W^T, the tile read MN-major, and frees the tile a
+//     quarter of the dims at a time.
+// The latent is never converted, and every wait is bounded: one that gives up
+// sets SML_FAULT_TIMEOUT and the CTA winds down.
+//
+// What bounds it, and what it measured (B200, 6.57 TB/s copy):
+//   * 16 heads, 32 contexts of 8K to 64K tokens: HBM.  147 us for 787 MB, 5.4
+//     TB/s; bf16 rows of the same batch 224 us, 94 % of the copy rate.  A tile
+//     takes 2.0 us against 1.9 of a 148th of that rate; the rest is 15 us before
+//     and 12 after the loop (first loads, uneven finish, join).
+//   * 128 heads, 32 tokens of 60,000 (four groups of 32 heads, which read a tile
+//     from L2 after the first): 940 us, 570 TFLOP/s of the attention's own.  The
+//     two buffers' cycle bounds it: load 0.75 us, QK^T 0.6, softmax 1.2, PV 0.5
+//     and the hand-overs between them, 4.6 us for two tiles; no unit is busy (issue
+//     56 %, shared memory's banks 34 %, L2 35 %).  A third buffer does not fit
+//     beside the query and the weights (224 KB), nor 64 heads' O and logits in
+//     TMEM; weights handed to PV in two waves, two loading warps, and raising M_h
+//     further at a time changed nothing.
+//   * few tiles a CTA (selected blocks, one short context): the chain of first
+//     loads, first tile, output and join, 15 us at least.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -491,54 +525,55 @@ __device__ __forceinline__ void stage_query(const Params& P, Smem<kFmt, kHU>& S,
     }
     if (p == 0) S.qs[h] = 1.f;
   } else {
-  uint4 v[4];
+    uint4 v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const uint4*>(qh + 32 * p) + i);
-  uint2 pv = make_uint2(0u, 0u);
-  if (P.rope_dim) pv = __ldcg(reinterpret_cast<const uint2*>(qh + SML_LATENT_DIM + 4 * p));
-  auto amax2 = [](uint32_t w) { return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))); };
-  float amax = 0.f;
+    for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const uint4*>(qh + 32 * p) + i);
+    uint2 pv = make_uint2(0u, 0u);
+    if (P.rope_dim) pv = __ldcg(reinterpret_cast<const uint2*>(qh + SML_LATENT_DIM + 4 * p));
+    auto amax2 = [](uint32_t w) { return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))); };
+    float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    amax = fmaxf(amax, fmaxf(fmaxf(amax2(v[i].x), amax2(v[i].y)), fmaxf(amax2(v[i].z), amax2(v[i].w))));
-  if (F::kPlain) amax = fmaxf(amax, fmaxf(amax2(pv.x), amax2(pv.y)));
+    for (int i = 0; i < 4; ++i)
+      amax = fmaxf(amax, fmaxf(fmaxf(amax2(v[i].x), amax2(v[i].y)), fmaxf(amax2(v[i].z), amax2(v[i].w))));
+    if (F::kPlain) amax = fmaxf(amax, fmaxf(amax2(pv.x), amax2(pv.y)));
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  int e2 = 0;
-  if (amax > 0.f) frexpf(amax / 448.f, &e2);   // amax / 448 < 2^e2
-  const float inv = ldexpf(1.f, -e2);
-  if (p == 0) S.qs[h] = ldexpf(1.f, e2);
-  auto split4 = [&](uint32_t wa, uint32_t wb, uint32_t& hi, uint32_t& lo) {
-    float x0 = __uint_as_float(wa << 16) * inv, x1 = __uint_as_float(wa & 0xffff0000u) * inv;
-    float x2 = __uint_as_float(wb << 16) * inv, x3 = __uint_as_float(wb & 0xffff0000u) * inv;
-    hi = split_e4m3x2(x0, x1);
-    hi |= split_e4m3x2(x2, x3) << 16;
-    lo = f2_to_e4m3x2(x0, x1) | (f2_to_e4m3x2(x2, x3) << 16);
-  };
-  // dims [32 p, 32 p + 32) -> block p / 4, 16-B chunks 2 (p % 4) and 2 (p % 4) + 1
-  const uint32_t qb = q0 + (p >> 2) * (2 * kHU * 128);
+    for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    int e2 = 0;
+    if (amax > 0.f) frexpf(amax / 448.f, &e2);   // amax / 448 < 2^e2
+    e2 = max(e2, -120);                          // 2^-e2 stays finite; such a query's logits are 0 either way
+    const float inv = ldexpf(1.f, -e2);
+    if (p == 0) S.qs[h] = ldexpf(1.f, e2);
+    auto split4 = [&](uint32_t wa, uint32_t wb, uint32_t& hi, uint32_t& lo) {
+      float x0 = __uint_as_float(wa << 16) * inv, x1 = __uint_as_float(wa & 0xffff0000u) * inv;
+      float x2 = __uint_as_float(wb << 16) * inv, x3 = __uint_as_float(wb & 0xffff0000u) * inv;
+      hi = split_e4m3x2(x0, x1);
+      hi |= split_e4m3x2(x2, x3) << 16;
+      lo = f2_to_e4m3x2(x0, x1) | (f2_to_e4m3x2(x2, x3) << 16);
+    };
+    // dims [32 p, 32 p + 32) -> block p / 4, 16-B chunks 2 (p % 4) and 2 (p % 4) + 1
+    const uint32_t qb = q0 + (p >> 2) * (2 * kHU * 128);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t hw[4], lw[4];
-    split4(v[2 * c].x, v[2 * c].y, hw[0], lw[0]);
-    split4(v[2 * c].z, v[2 * c].w, hw[1], lw[1]);
-    split4(v[2 * c + 1].x, v[2 * c + 1].y, hw[2], lw[2]);
-    split4(v[2 * c + 1].z, v[2 * c + 1].w, hw[3], lw[3]);
-    const int chunk = 2 * (p & 3) + c;
-    const bool split = F::split_terms(kHU, p >> 2);
-    st_v4(sw128(qb, split ? split_col<kHU>(h, 0) : h, chunk), hw[0], hw[1], hw[2], hw[3]);
-    st_v4(sw128(qb, split ? split_col<kHU>(h, 1) : h + kHU, chunk), lw[0], lw[1], lw[2], lw[3]);
-  }
-  if (P.rope_dim) {
-    if (F::kPlain) {
-      uint32_t hi, lo;
-      split4(pv.x, pv.y, hi, lo);
-      st_b32(sw128(qp, split_col<kHU>(h, 0), p >> 2) + 4 * (p & 3), hi);
-      st_b32(sw128(qp, split_col<kHU>(h, 1), p >> 2) + 4 * (p & 3), lo);
-    } else {
-      st_v2(sw128(qp, h, p >> 1) + 8 * (p & 1), pv.x, pv.y);
+    for (int c = 0; c < 2; ++c) {
+      uint32_t hw[4], lw[4];
+      split4(v[2 * c].x, v[2 * c].y, hw[0], lw[0]);
+      split4(v[2 * c].z, v[2 * c].w, hw[1], lw[1]);
+      split4(v[2 * c + 1].x, v[2 * c + 1].y, hw[2], lw[2]);
+      split4(v[2 * c + 1].z, v[2 * c + 1].w, hw[3], lw[3]);
+      const int chunk = 2 * (p & 3) + c;
+      const bool split = F::split_terms(kHU, p >> 2);
+      st_v4(sw128(qb, split ? split_col<kHU>(h, 0) : h, chunk), hw[0], hw[1], hw[2], hw[3]);
+      st_v4(sw128(qb, split ? split_col<kHU>(h, 1) : h + kHU, chunk), lw[0], lw[1], lw[2], lw[3]);
     }
-  }
+    if (P.rope_dim) {
+      if (F::kPlain) {
+        uint32_t hi, lo;
+        split4(pv.x, pv.y, hi, lo);
+        st_b32(sw128(qp, split_col<kHU>(h, 0), p >> 2) + 4 * (p & 3), hi);
+        st_b32(sw128(qp, split_col<kHU>(h, 1), p >> 2) + 4 * (p & 3), lo);
+      } else {
+        st_v2(sw128(qp, h, p >> 1) + 8 * (p & 1), pv.x, pv.y);
+      }
+    }
   }
 }
 

@@ -132,6 +132,24 @@ def test_flat_and_peaked_softmax(fmt, gain):
     check_all(f"{fmt} gain {gain}", wl, out, lse)
 
 
+@pytest.mark.parametrize("fmt", ["fp8_ds_mla", "e4m3", "bf16"])
+def test_smallest_and_largest_queries(fmt):
+    """Heads of zeros, of bf16's smallest magnitudes among zeros, and of magnitudes near its largest
+    (kept finite by sm_scale)."""
+    wl = synth.make_workload(f"paged/extreme/{fmt}", [200], [1], 16, latent_format=fmt, layers=(("l", 64, False, None),))
+    q = (wl.layers[0].q.astype(np.uint32) << 16).view(np.float32)
+    q[0, 0] = 0.0
+    q[0, 1] *= np.float32(2.0 ** -126)
+    q[0, 1, ::3] = 0.0
+    q[0, 2] = np.where(np.arange(576) == 7, np.float32(2.0 ** -133), 0.0)
+    q[0, 3] *= np.float32(2.0 ** 120)
+    q[0, 4:] *= np.float32(2.0 ** 118)
+    wl.layers[0].q = synth.to_bf16_bits(q)
+    wl.sm_scale = float(np.float32(2.0 ** -122))
+    out, lse = paged(wl)
+    check_all(fmt, wl, out, lse)
+
+
 def test_rising_logits():
     """Keys that grow along the context: every tile raises the running maximum."""
     wl = synth.make_workload("paged/rise", [1500], [1], 16, latent_format="bf16", layers=(("l", 64, False, None),))
