@@ -29,12 +29,12 @@
 // sets SML_FAULT_TIMEOUT and the CTA winds down.
 //
 // What bounds it, and what it measured (B200, 6.57 TB/s copy):
-//   * 16 heads, 32 contexts of 8K to 64K tokens: HBM.  147 us for 787 MB, 5.4
+//   * 16 heads, 32 contexts of 8K to 64K tokens: HBM.  143 us for 787 MB, 5.5
 //     TB/s; bf16 rows of the same batch 224 us, 94 % of the copy rate.  A tile
-//     takes 2.0 us against 1.9 of a 148th of that rate; the rest is 15 us before
-//     and 12 after the loop (first loads, uneven finish, join).
+//     takes 2.0 us against 1.9 of a 148th of that rate; the rest is what stands
+//     before and after the loop (first loads, uneven finish, join).
 //   * 128 heads, 32 tokens of 60,000 (four groups of 32 heads, which read a tile
-//     from L2 after the first): 940 us, 570 TFLOP/s of the attention's own.  The
+//     from L2 after the first): 906 us, 590 TFLOP/s of the attention's own.  The
 //     two buffers' cycle bounds it: load 0.75 us, QK^T 0.6, softmax 1.2, PV 0.5
 //     and the hand-overs between them, 4.6 us for two tiles; no unit is busy (issue
 //     56 %, shared memory's banks 34 %, L2 35 %).  A third buffer does not fit
@@ -42,7 +42,9 @@
 //     TMEM; weights handed to PV in two waves, two loading warps, and raising M_h
 //     further at a time changed nothing.
 //   * few tiles a CTA (selected blocks, one short context): the chain of first
-//     loads, first tile, output and join, 15 us at least.
+//     loads, first tile, output and join, 14 us at least.  Code that a CTA runs
+//     once or twice costs what it takes to fetch, 0.5 to 0.9 us for 2 to 3 KB of
+//     it unrolled, so there a lane works for all (rebase, the row sums).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -71,10 +73,6 @@ constexpr uint32_t kColO = 256;          // TMEM: logits from column 0, O from h
 constexpr float kNoM = -1e30f;            // M_h before a head's first key: any logit is far above it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Weight exponents: a weight is capped at 440 (E4M3's largest value is 448;
-// the margin covers the approximate 2^x and log2).
-constexpr float kLog2Cap = 8.78135971f;    // log2(440)
-constexpr float kLog2Head = 6.80735492f;   // log2(112)
 template <int kHU>
 constexpr int kGroupBf = 2 * kHU * 2 * 8;  // bytes of an 8-key group of bf16 weights
 
@@ -351,7 +349,8 @@ struct __align__(1024) Smem {
   uint8_t pb[kOwnSets][kSetBytes];                // weight sets: 8-key x 16-B core matrices
   float sc[F::kDs ? F::kBufs : 1][kKT][4];        // [buffer][key] block scales
   __align__(8) float xmax[4][4][kHU / 4];                      // [head quarter][key quarter][head]
-  float xscale[4][4][4];                          // [head quarter][key quarter][block]
+  __align__(16) float xscale[4][4][4];            // [head quarter][key quarter][block]
+  __align__(8) float nm[16][kHU / 4], fac[16][kHU / 4];   // [warp][head] -M_h, and what O scales by
   __align__(8) float xsum[4][4][kHU / 4];
   float qs[kHU];                                  // power-of-two query scale per head
   int4 rows[4];                                   // [tile % 4] valid rows {lo, hi} of each page of the tile
@@ -429,6 +428,10 @@ __device__ __forceinline__ void st_b32(uint32_t addr, uint32_t a) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
 
+__device__ __forceinline__ void st_b16(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"((uint16_t)a) : "memory");
+}
+
 __device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
 }
@@ -465,6 +468,9 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// 2^e: 0 below the smallest normal number, at most 2^127.
+__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __int_as_float((127 + min(e, 127)) << 23); }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
   return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
@@ -506,75 +512,238 @@ __device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[4]) { ptx::tm
 __device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[8]) { ptx::tmem_ld8(a, r); }
 __device__ __forceinline__ void tmem_stn(uint32_t a, const uint32_t (&r)[8]) { ptx::tmem_st8(a, r); }
 
-// Stage the query of (token t, head group g); thread = head x 32-dim part of
-// 16.  E4M3 pools: q = s_h (hi + lo), both E4M3, s_h the power of two >= amax_h
-// / 448: exact wherever |q| >= 2^-6 s_h (a bf16 has 8 significant bits, four
-// in each term), else within 2^-10 s_h.  RoPE: bf16 as given (fp8_ds_mla), or
-// split the same way (plain E4M3).  bf16 pools: the bf16 query as given.
+// Stage the query of (token t, head group g); thread = head x 1 / kPer of its
+// latent dims and RoPE dims.  E4M3 pools: q = s_h (hi + lo), both E4M3, s_h the
+// power of two with amax_h <= 448 s_h: exact wherever |q| >= 2^-6 s_h (a bf16 has
+// 8 significant bits, four in each term), else within 2^-10 s_h.  RoPE: bf16 as
+// given (fp8_ds_mla), or split the same way (plain E4M3).  bf16 pools: the bf16
+// query as given.
 template <int kFmt, int kHU>
 __device__ __forceinline__ void stage_query(const Params& P, Smem<kFmt, kHU>& S, int t, int g, int tid) {
   using F = Fmt<kFmt>;
-  const int h = tid >> 4, p = tid & 15;
+  constexpr int kPer = kSoftmaxThreads / kHU;          // threads a head: 32 or 16
+  constexpr int kChunks = SML_LATENT_DIM / kPer / 16;   // 16-dim chunks a thread: 1 or 2
+  const int h = tid / kPer, p = tid % kPer;
   const uint16_t* qh = P.q + ((size_t)t * P.H + g * kHU + h) * (SML_LATENT_DIM + P.rope_dim);
   const uint32_t q0 = ptx::smem_u32(S.q8), qp = ptx::smem_u32(S.qpe);
   if constexpr (F::kBf) {
     const int nc = P.rope_dim ? 72 : 64;
-    for (int c = p; c < nc; c += 16) {
+    for (int c = p; c < nc; c += kPer) {
       const uint4 v = __ldcg(reinterpret_cast<const uint4*>(qh) + c);
       st_v4(c < 64 ? sw128(q0 + (c >> 3) * (kHU * 128), h, c & 7) : sw128(qp, h, c - 64), v.x, v.y, v.z, v.w);
     }
     if (p == 0) S.qs[h] = 1.f;
   } else {
-    uint4 v[4];
+    uint4 v[2 * kChunks];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const uint4*>(qh + 32 * p) + i);
-    uint2 pv = make_uint2(0u, 0u);
-    if (P.rope_dim) pv = __ldcg(reinterpret_cast<const uint2*>(qh + SML_LATENT_DIM + 4 * p));
-    auto amax2 = [](uint32_t w) { return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))); };
-    float amax = 0.f;
+    for (int i = 0; i < 2 * kChunks; ++i) v[i] = __ldcg(reinterpret_cast<const uint4*>(qh) + 2 * kChunks * p + i);
+    constexpr int kPe = 64 / kPer / 2;   // pairs of RoPE dims a thread: 1 or 2
+    uint32_t pv[kPe] = {};
+    if (P.rope_dim) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      amax = fmaxf(amax, fmaxf(fmaxf(amax2(v[i].x), amax2(v[i].y)), fmaxf(amax2(v[i].z), amax2(v[i].w))));
-    if (F::kPlain) amax = fmaxf(amax, fmaxf(amax2(pv.x), amax2(pv.y)));
+      for (int i = 0; i < kPe; ++i) pv[i] = __ldcg(reinterpret_cast<const uint32_t*>(qh + SML_LATENT_DIM) + kPe * p + i);
+    }
+    // amax as the largest bit pattern without sign
+    uint32_t m2 = 0;
+    auto amax2 = [&](uint32_t w) { m2 = __vmaxu2(m2, w & 0x7fff7fffu); };
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    int e2 = 0;
-    if (amax > 0.f) frexpf(amax / 448.f, &e2);   // amax / 448 < 2^e2
-    e2 = max(e2, -120);                          // 2^-e2 stays finite; such a query's logits are 0 either way
-    const float inv = ldexpf(1.f, -e2);
-    if (p == 0) S.qs[h] = ldexpf(1.f, e2);
-    auto split4 = [&](uint32_t wa, uint32_t wb, uint32_t& hi, uint32_t& lo) {
-      float x0 = __uint_as_float(wa << 16) * inv, x1 = __uint_as_float(wa & 0xffff0000u) * inv;
-      float x2 = __uint_as_float(wb << 16) * inv, x3 = __uint_as_float(wb & 0xffff0000u) * inv;
+    for (int i = 0; i < 2 * kChunks; ++i) {
+      amax2(v[i].x);
+      amax2(v[i].y);
+      amax2(v[i].z);
+      amax2(v[i].w);
+    }
+    if (F::kPlain) {
+#pragma unroll
+      for (int i = 0; i < kPe; ++i) amax2(pv[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < kPer; o <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    const int amax = max((int)(m2 & 0xffffu), (int)(m2 >> 16));
+    // 448 = 1.75 * 2^8; 2^-e2 stays finite (a query that small gives logits of 0 either way)
+    const int e2 = max((amax >> 7) - 127 - 8 + ((amax & 127) > 96), -120);
+    const float inv = __int_as_float((127 - e2) << 23);
+    if (p == 0) S.qs[h] = amax < 0x7f80 ? __int_as_float((127 + e2) << 23) : NAN;   // infinities would be clipped
+    auto split2 = [&](uint32_t w, uint32_t& hi, uint32_t& lo) {
+      float x0 = __uint_as_float(w << 16) * inv, x1 = __uint_as_float(w & 0xffff0000u) * inv;
       hi = split_e4m3x2(x0, x1);
-      hi |= split_e4m3x2(x2, x3) << 16;
-      lo = f2_to_e4m3x2(x0, x1) | (f2_to_e4m3x2(x2, x3) << 16);
+      lo = f2_to_e4m3x2(x0, x1);
     };
-    // dims [32 p, 32 p + 32) -> block p / 4, 16-B chunks 2 (p % 4) and 2 (p % 4) + 1
-    const uint32_t qb = q0 + (p >> 2) * (2 * kHU * 128);
+    auto split4 = [&](uint32_t wa, uint32_t wb, uint32_t& hi, uint32_t& lo) {
+      uint32_t h2, l2;
+      split2(wa, hi, lo);
+      split2(wb, h2, l2);
+      hi |= h2 << 16;
+      lo |= l2 << 16;
+    };
+    // dims [16 kChunks p, ..) -> block p / (kPer / 4), 16-B chunks kChunks (p % (kPer / 4)) ..
+    const int blk = p / (kPer / 4);
+    const uint32_t qb = q0 + blk * (2 * kHU * 128);
+    const bool split = F::split_terms(kHU, blk);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kChunks; ++c) {
       uint32_t hw[4], lw[4];
       split4(v[2 * c].x, v[2 * c].y, hw[0], lw[0]);
       split4(v[2 * c].z, v[2 * c].w, hw[1], lw[1]);
       split4(v[2 * c + 1].x, v[2 * c + 1].y, hw[2], lw[2]);
       split4(v[2 * c + 1].z, v[2 * c + 1].w, hw[3], lw[3]);
-      const int chunk = 2 * (p & 3) + c;
-      const bool split = F::split_terms(kHU, p >> 2);
+      const int chunk = kChunks * (p % (kPer / 4)) + c;
       st_v4(sw128(qb, split ? split_col<kHU>(h, 0) : h, chunk), hw[0], hw[1], hw[2], hw[3]);
       st_v4(sw128(qb, split ? split_col<kHU>(h, 1) : h + kHU, chunk), lw[0], lw[1], lw[2], lw[3]);
     }
     if (P.rope_dim) {
-      if (F::kPlain) {
-        uint32_t hi, lo;
-        split4(pv.x, pv.y, hi, lo);
-        st_b32(sw128(qp, split_col<kHU>(h, 0), p >> 2) + 4 * (p & 3), hi);
-        st_b32(sw128(qp, split_col<kHU>(h, 1), p >> 2) + 4 * (p & 3), lo);
-      } else {
-        st_v2(sw128(qp, h, p >> 1) + 8 * (p & 1), pv.x, pv.y);
+#pragma unroll
+      for (int i = 0; i < kPe; ++i) {
+        const int at = kPe * p + i;   // pair of dims
+        if (F::kPlain) {
+          uint32_t hi, lo;
+          split2(pv[i], hi, lo);
+          st_b16(sw128(qp, split_col<kHU>(h, 0), at >> 3) + 2 * (at & 7), hi);
+          st_b16(sw128(qp, split_col<kHU>(h, 1), at >> 3) + 2 * (at & 7), lo);
+        } else {
+          st_b32(sw128(qp, h, at >> 2) + 4 * (at & 3), pv[i]);
+        }
       }
     }
   }
+}
+
+// Weights are capped at 440 (E4M3's largest value is 448; the margin covers the
+// approximate 2^x and log2) and set to at most 112.  bf16 weights need no such
+// range: M_h only keeps them within 2^16.
+template <int kFmt>
+constexpr float kCap = kFmt == kFmtBf16 ? 16.f : 8.78135971f;    // log2(440)
+template <int kFmt>
+constexpr float kHead = kFmt == kFmtBf16 ? 0.f : 6.80735492f;    // log2(112)
+constexpr float kFar = 50.f;   // a block scale 2^kFar above 2^eb raises eb whatever its key's weight: lk stays finite
+
+// log2 of a key's largest block scale, relative to 2^eb of its block.
+__device__ __forceinline__ float log_rel(const float (&sc)[4], const float (&ebf)[4]) {
+  const float top = fmaxf(fmaxf(sc[0] * ebf[0], sc[1] * ebf[1]), fmaxf(sc[2] * ebf[2], sc[3] * ebf[3]));
+  return lg2(fminf(fmaxf(top, 0x1p-60f), 0x1p100f));
+}
+
+// The exponents that the weights of a tile need, for the four warps of a head
+// quarter (its heads, this thread's key), and what has been summed up so far in
+// units of the new ones.  A lane works out one head's, or one block's, and all
+// read it back: this code is run once in a while, and fetched for it (with every
+// thread working out all of them, unrolled, a pass took 0.9 us more).
+//
+// A head whose largest softmax weight of the tile is above 2^limit takes the
+// integer M_h that puts it in (56, 112]: headroom of 4 for later tiles, and the
+// dominant weights keep all eight bits.  Then the same for each block's weight
+// times scale, over the quarter's heads: the first tile sets eb, one that passes
+// the cap all the same raises it, and it may fall by as much as every M_h has
+// risen (what O holds is that much smaller).  O scales by powers of two, exactly.
+//
+// In: z the logits + lk; out: z less M_h.  last: the tile whose PV O waits for;
+// -1 where O holds nothing yet.
+template <int kFmt, int kHU, int kHP>
+__device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], float2 (&nM)[kHP], float2 (&lrow)[kHP],
+                                       const float (&scv)[4], float (&ebf)[4], float& lk, uint32_t T0, int last) {
+  using F = Fmt<kFmt>;
+  constexpr int kHT = kHU / 4, kFirst = 1000;
+  constexpr float kLimit = F::kDs ? kHead<kFmt> + 1.f : kCap<kFmt>;   // (the block's scale may come on top)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, hq = warp >> 2;
+  // this thread's latent dim of output block 0, this quarter's heads
+  const uint32_t o_addr = T0 + kColO + 2 * kHT * hq + ((uint32_t)(32 * q4) << 16);
+  if constexpr (F::kDs) {
+#pragma unroll
+    for (int i = 0; i < kHP; ++i) z[i] = __fadd2_rn(z[i], make_float2(-lk, -lk));
+  }
+#pragma unroll
+  for (int i = 0; i < kHP; ++i) {
+    const float a = ptx::warp_max_f32(z[i].x), b = ptx::warp_max_f32(z[i].y);
+    if (lane == 0) *reinterpret_cast<float2*>(&S.xmax[hq][q4][2 * i]) = make_float2(a, b);
+  }
+  group_sync(hq);
+  int rise;   // the least that any of the quarter's M_h rises by
+  {
+    const int h = lane % kHT;
+    const float e = fmaxf(fmaxf(S.xmax[hq][0][h], S.xmax[hq][1][h]), fmaxf(S.xmax[hq][2][h], S.xmax[hq][3][h]));
+    float neg = S.nm[warp][h];
+    const bool was = neg != -kNoM;
+    int by = 0;
+    if (e + neg > kLimit) {
+      const float Mn = ceilf(e - kHead<kFmt>);
+      by = (int)fminf(Mn + neg, 500.f);   // a positive integer (of a head without M_h: any)
+      neg = -Mn;
+    }
+    if (lane < kHT) {
+      S.nm[warp][h] = neg;
+      S.fac[warp][h] = was ? pow2(-by) : 1.f;
+    }
+    rise = __reduce_min_sync(0xffffffffu, was ? by : kFirst);
+    const bool any = __any_sync(0xffffffffu, was && by > 0);   // (also makes the stores visible to the warp)
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kHP; ++i) {
+      nM[i] = *reinterpret_cast<const float2*>(&S.nm[warp][2 * i]);
+      lrow[i] = __fmul2_rn(lrow[i], *reinterpret_cast<const float2*>(&S.fac[warp][2 * i]));
+      z[i] = __fadd2_rn(z[i], nM[i]);
+    }
+    if (any && last >= 0) {
+      if (!warp_wait(&S.pv_done, last & 1, &S.abort)) return false;   // the last tile's PV accumulates into O
+      ptx::tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        uint32_t ov[2 * kHT];
+        tmem_ldn(o_addr + 2 * kHU * b, ov);
+        ptx::tmem_wait_ld(ov);
+#pragma unroll
+        for (int i = 0; i < kHT; ++i) {
+          const float fi = S.fac[warp][i];
+          ov[i] = __float_as_uint(__uint_as_float(ov[i]) * fi);
+          ov[kHT + i] = __float_as_uint(__uint_as_float(ov[kHT + i]) * fi);
+        }
+        tmem_stn(o_addr + 2 * kHU * b, ov);
+      }
+      ptx::tmem_wait_st();
+    }
+  }
+  if constexpr (F::kDs) {
+    float u = -kFar;
+#pragma unroll
+    for (int i = 0; i < kHP; ++i) u = fmaxf(u, fmaxf(z[i].x, z[i].y));
+    if (rise >= 4 || group_any(hq, u + lk > kCap<kFmt>)) {
+      float v[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) v[b] = ptx::warp_max_f32(u + lg2(scv[b]));
+      if (lane == 0) *reinterpret_cast<float4*>(S.xscale[hq][q4]) = make_float4(v[0], v[1], v[2], v[3]);
+      group_sync(hq);
+      const int b = lane & 3;
+      const float t = fmaxf(fmaxf(S.xscale[hq][0][b], S.xscale[hq][1][b]), fmaxf(S.xscale[hq][2][b], S.xscale[hq][3][b]));
+      const float was = b & 2 ? (b & 1 ? ebf[3] : ebf[2]) : (b & 1 ? ebf[1] : ebf[0]);
+      const int eb = 127 - (int)(__float_as_uint(was) >> 23);
+      const int fit = (int)ceilf(fminf(fmaxf(t - kHead<kFmt>, -126.f), 126.f));
+      const int to = rise == kFirst               ? fit
+                     : t - (float)eb > kCap<kFmt> ? max(fit, eb)
+                                                  : max(min(fit, eb), eb - min(rise, 64));
+      const float now = pow2(-to);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ebf[i] = __shfl_sync(0xffffffffu, now, i);
+      if (last >= 0 && __any_sync(0xffffffffu, to != eb)) {
+        const float f = pow2(eb - to);
+        if (!warp_wait(&S.pv_done, last & 1, &S.abort)) return false;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, f, i);
+          uint32_t ov[2 * kHT];
+          tmem_ldn(o_addr + 2 * kHU * i, ov);
+          ptx::tmem_wait_ld(ov);
+#pragma unroll
+          for (int h = 0; h < 2 * kHT; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * fi);
+          tmem_stn(o_addr + 2 * kHU * i, ov);
+        }
+        ptx::tmem_wait_st();
+      }
+      lk = log_rel(scv, ebf);
+    }
+#pragma unroll
+    for (int i = 0; i < kHP; ++i) z[i] = __fadd2_rn(z[i], make_float2(lk, lk));
+  }
+  return true;
 }
 
 template <int kFmt, int kHU>
@@ -594,7 +763,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       ptx::mbar_init(&S.full[0][0] + i, 1);
       ptx::mbar_init(&S.lat_free[0][0] + i, 1);
     }
-    ptx::mbar_init(&S.q_ready, 16 * kHU / 32);
+    ptx::mbar_init(&S.q_ready, kSoftmaxWarps);
     ptx::mbar_init(&S.s_full, 1);
     ptx::mbar_init(&S.s_free, kSoftmaxWarps);
     ptx::mbar_init(&S.p_full, kSoftmaxWarps);
@@ -844,14 +1013,11 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     // quarter: this thread owns key (or dim) `row` for heads kHT hq ..
     const int q4 = warp & 3, hq = warp >> 2, row = 32 * q4 + lane, tid = threadIdx.x;
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    constexpr int kStageWarps = 16 * kHU / 32;
     auto stage = [&](const Seg& s) {
-      if (warp < kStageWarps) {
-        stage_query<kFmt, kHU>(P, S, s.t, g, tid);
-        ptx::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&S.q_ready);
-      }
+      stage_query<kFmt, kHU>(P, S, s.t, g, tid);
+      ptx::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.q_ready);
     };
     Walk w = begin;
     Seg s;
@@ -885,10 +1051,10 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         nM[i] = make_float2(-kNoM, -kNoM);
         lrow[i] = make_float2(0.f, 0.f);
       }
-      // Block scales enter the weights relative to 2^eb, the largest of the
-      // block in the piece's first tile, so that blocks of different magnitude
-      // all use E4M3's range; the output is multiplied back.
-      float ebf[4] = {1.f, 1.f, 1.f, 1.f}, ebi[4] = {1.f, 1.f, 1.f, 1.f};
+      if (lane < kHT) S.nm[warp][lane] = -kNoM;
+      // A block's scales enter the weights relative to 2^eb, so that every block
+      // uses E4M3's range whatever its magnitude; the output is multiplied back.
+      float ebf[4] = {1.f, 1.f, 1.f, 1.f};   // 2^-eb
       for (int jj = 0; jj < s.ne; ++jj, ++k) {
         const int buf = k % kBufs;
         ok = ok && warp_wait(&S.full[buf][kRopePart], (k / kBufs) & 1, abort) && warp_wait(&S.s_full, k & 1, abort);
@@ -910,23 +1076,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           scv[2] = f.z;
           scv[3] = f.w;
           if (partial && !valid) scv[0] = scv[1] = scv[2] = scv[3] = 0.f;
-          if (jj == 0) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const float x = ptx::warp_max_f32(scv[b]);
-              if (lane == 0) S.xscale[hq][q4][b] = x;
-            }
-            group_sync(hq);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const float x = fmaxf(fmaxf(S.xscale[hq][0][b], S.xscale[hq][1][b]), fmaxf(S.xscale[hq][2][b], S.xscale[hq][3][b]));
-              const int e = min(max((int)((__float_as_uint(x) >> 23) & 255) - 127, -100), 100);
-              ebf[b] = __int_as_float((127 - e) << 23);
-              ebi[b] = __int_as_float((127 + e) << 23);
-            }
-          }
-          const float top = fmaxf(fmaxf(scv[0] * ebf[0], scv[1] * ebf[1]), fmaxf(scv[2] * ebf[2], scv[3] * ebf[3]));
-          lk = lg2(fmaxf(top, 0x1p-60f));
+          lk = log_rel(scv, ebf);
           rk = ex2(-lk);
           float2 acc[kHP];
 #pragma unroll
@@ -990,9 +1140,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         }
         // The weights 2^(z - M_h) must stay within E4M3's 448.  One above the
         // cap, or a head without M_h yet, sends the quarter's four warps through
-        // the exact update (a vote: rare after the first tile).  bf16: M_h only
-        // keeps 2^(z - M_h) within 2^16.
-        constexpr float kCap = F::kBf ? 16.f : kLog2Cap, kHead = F::kBf ? 0.f : kLog2Head;
+        // the exact update (a vote: rare after the first tile).
         float2 d[kHP];
         float most = -INFINITY;
 #pragma unroll
@@ -1000,68 +1148,27 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
           d[i] = __fadd2_rn(z[i], nM[i]);
           most = fmaxf(most, fmaxf(d[i].x, d[i].y));
         }
-        bool need = group_any(hq, most > kCap || !ok);
-        float2 f[kHP];
-        bool any = false;
-        if (need) {
-          ok = !group_any(hq, !ok);   // a wait that gave up ends the quarter's warps together
-          if (!ok) break;
-          // A head whose largest weight of this tile passes the cap takes the
-          // integer M_h that puts it in (56, 112]: headroom of 4 for later
-          // tiles, and the dominant weights keep all eight bits.  O and the
-          // row sums scale by 2^(M_old - M_new), exactly.
-#pragma unroll
-          for (int i = 0; i < kHP; ++i) {
-            const float x = ptx::warp_max_f32(z[i].x), y = ptx::warp_max_f32(z[i].y);
-            if (lane == 0) *reinterpret_cast<float2*>(&S.xmax[hq][q4][2 * i]) = make_float2(x, y);
+        if (F::kDs) most = fmaxf(most, lk - kFar);
+        if (group_any(hq, most > kCap<kFmt> || !ok)) {
+          if (group_any(hq, !ok)) {   // a wait that gave up ends the quarter's warps together
+            ok = false;
+            break;
           }
-          group_sync(hq);
-          auto raise = [&](float e, float& neg, float& fac) {   // e: the tile's largest z of a head
-            fac = 1.f;
-            if (!(e + neg > kCap)) return;
-            const float Mn = ceilf(e - kHead);
-            if (neg != -kNoM) {
-              const float by = -neg - Mn;   // a negative integer
-              fac = by < -126.f ? 0.f : __int_as_float((127 + (int)by) << 23);
-              any = true;
-            }
-            neg = -Mn;
-          };
-#pragma unroll
-          for (int i = 0; i < kHP; ++i) {
-            float2 e = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-            for (int qq = 0; qq < 4; ++qq) {
-              const float2 x = *reinterpret_cast<const float2*>(&S.xmax[hq][qq][2 * i]);
-              e = make_float2(fmaxf(e.x, x.x), fmaxf(e.y, x.y));
-            }
-            raise(e.x, nM[i].x, f[i].x);
-            raise(e.y, nM[i].y, f[i].y);
-            lrow[i] = __fmul2_rn(lrow[i], f[i]);
-            d[i] = __fadd2_rn(z[i], nM[i]);
+          ok = rebase<kFmt, kHU>(S, z, nM, lrow, scv, ebf, lk, T0, jj > 0 ? k - 1 : -1);
+          if (!ok) {
+            *abort = 1;
+            continue;   // the next vote ends the quarter's warps
           }
+          rk = ex2(-lk);
+#pragma unroll
+          for (int i = 0; i < kHP; ++i) d[i] = z[i];
         }
-        // The last tile's PV reads the weights and accumulates into O: it is
-        // waited for before either changes (of the piece before, by its epilogue).
+        // the last tile's PV reads the weights (of the piece before: its epilogue waited)
         if (jj > 0) {
           ok = warp_wait(&S.pv_done, (k - 1) & 1, abort);
           if (!ok) {
             *abort = 1;
             continue;   // the next vote ends the quarter's warps
-          }
-          if (any) {
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {   // this thread's latent dim of block b, this quarter's heads
-              uint32_t ov[2 * kHT];
-              const uint32_t a = T0 + kColO + 2 * kHU * b + 2 * kHT * hq + lane_off;
-              tmem_ldn(a, ov);
-              ptx::tmem_wait_ld(ov);
-#pragma unroll
-              for (int h = 0; h < 2 * kHT; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * (h & 1 ? f[h % kHT / 2].y : f[h % kHT / 2].x));
-              tmem_stn(a, ov);
-            }
-            ptx::tmem_wait_st();
           }
         }
         // p: the weights times this key's largest scale
@@ -1145,38 +1252,51 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
       ok = softmax_all(ok);
       if (!ok) break;
       ptx::tc_fence_after();
+      // Row sums over the keys: halving the heads with each exchange, a lane is
+      // left with head lane / (32 / kHT); then a lane a head, see rebase.
+      float v[kHT];
 #pragma unroll
       for (int i = 0; i < kHP; ++i) {
-        float2 v = lrow[i];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-          v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        }
-        if (lane == 0) *reinterpret_cast<float2*>(&S.xsum[hq][q4][2 * i]) = v;
+        v[2 * i] = lrow[i].x;
+        v[2 * i + 1] = lrow[i].y;
       }
+#pragma unroll
+      for (int n = kHT / 2, o = 16; o > 0; n /= 2, o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < (n > 0 ? n : 1); ++i) {
+          const float mine = n > 0 && up ? v[i + n] : v[i], other = n > 0 && !up ? v[i + n] : v[i];
+          v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+        }
+      }
+      if (lane % (32 / kHT) == 0) S.xsum[hq][q4][lane / (32 / kHT)] = v[0];
       group_sync(hq);
+      {
+        const int h = lane % kHT;
+        const float l = S.xsum[hq][0][h] + S.xsum[hq][1][h] + S.xsum[hq][2][h] + S.xsum[hq][3][h];
+        if (lane < kHT) {
+          S.fac[warp][h] = l > 0.f ? (F::kPlain ? P.latent_scale : 1.f) / l : l == 0.f ? 0.f : l;   // NaN stays
+          if (q4 == 0) {
+            const float lse = l == 0.f ? -INFINITY : (log2f(l) - S.nm[warp][h]) * kLn2;
+            if (s.whole) P.lse[orow + kHT * hq + h] = lse;
+            else P.ws.part_lse[s.part + kHT * hq + h] = lse;
+          }
+        }
+        __syncwarp();
+      }
       float osc[kHT];
 #pragma unroll
-      for (int h = 0; h < kHT; ++h) {
-        const float l = S.xsum[hq][0][h] + S.xsum[hq][1][h] + S.xsum[hq][2][h] + S.xsum[hq][3][h];
-        osc[h] = l > 0.f ? (F::kPlain ? P.latent_scale : 1.f) / l : l == 0.f ? 0.f : l;   // NaN stays
-        if (q4 == 0 && lane == 0) {
-          const float lse = l == 0.f ? -INFINITY : (log2f(l) - (h & 1 ? nM[h / 2].y : nM[h / 2].x)) * kLn2;
-          if (s.whole) P.lse[orow + kHT * hq + h] = lse;
-          else P.ws.part_lse[s.part + kHT * hq + h] = lse;
-        }
-      }
+      for (int h = 0; h < kHT; ++h) osc[h] = S.fac[warp][h];
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {   // (not unrolled: its code is run once a piece, and fetched for it)
         uint32_t ov[2 * kHT];
         tmem_ldn(T0 + kColO + 2 * kHU * b + 2 * kHT * hq + lane_off, ov);
         ptx::tmem_wait_ld(ov);
         const int dim = 128 * b + row;
-        const float eb = b == 0 ? ebi[0] : b == 1 ? ebi[1] : b == 2 ? ebi[2] : ebi[3];
+        const float back = 1.f / (b == 0 ? ebf[0] : b == 1 ? ebf[1] : b == 2 ? ebf[2] : ebf[3]);   // a power of two
 #pragma unroll
         for (int h = 0; h < kHT; ++h) {
-          const float o = (__uint_as_float(ov[h]) + __uint_as_float(ov[kHT + h])) * osc[h] * eb;
+          const float o = (__uint_as_float(ov[h]) + __uint_as_float(ov[kHT + h])) * osc[h] * back;
           if (s.whole) {
             const __nv_bfloat16 r = __float2bfloat16_rn(o);
             P.out[(orow + kHT * hq + h) * SML_LATENT_DIM + dim] = *reinterpret_cast<const uint16_t*>(&r);
@@ -1234,7 +1354,7 @@ paged_join_kernel(int H, int heads, PagedWs ws, uint16_t* __restrict__ out, floa
   for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
   float den = 0.f;
   for (int i = tid; i < n; i += kJoinThreads) {
-    const float w = m == -INFINITY ? 0.f : expf(wt[i] - m);
+    const float w = wt[i] == -INFINITY ? 0.f : expf(wt[i] - m);   // NaN stays
     wt[i] = w;
     den += w;
   }

@@ -25,8 +25,34 @@ from tests import parity
 U = 2.0 ** -8
 
 
-def expect(wl, layer_i, t, positions, n=None, nss=None):
-    """(out, lse, out bound, lse bound) of token t over logical positions, in float64."""
+def block_scales(wl, pages, rows):
+    """[n, 4] block scales of rows of an fp8_ds_mla pool."""
+    return np.ascontiguousarray(wl.latent.reshape(-1, 656)[pages * 64 + rows, 512:528]).view("<f4").astype(np.float64)
+
+
+def small_weight_term(p, scales, c):
+    """The third bound for block scales of any spread, [H, 512].  Four heads (eight of 32 heads and
+    more) share a scale 2^eb for each block, set to put their largest weight of a 128-key tile,
+    p' sc_b / 2^eb_b with p' = p / 2^M_h, into (56, 112] by powers of two, raised for a tile above it;
+    M_h puts the largest p' of a tile into (56, 112] too.  So 2^M_h <= pmax_h / 56 and 2^eb_b <=
+    112 / 56 V_b, V_b the largest p_hi / (pmax_h of the tile) sc_ib of those heads over the tiles,
+    and half of E4M3's subnormal step in each of two terms is 2^-9 2^(M_h + eb_b) <=
+    2^-9 / 28 pmax_h V_b for a code of one."""
+    H, n = p.shape
+    w = np.zeros((H, 4))
+    for a in range(0, n, 128):
+        top = np.maximum(p[:, a:a + 128].max(1), 1e-300)
+        w = np.maximum(w, (p[:, a:a + 128, None] / top[:, None, None] * scales[None, a:a + 128]).max(1))
+    heads = 4 if H == 16 else 8
+    V = np.repeat(w.reshape(-1, heads, 4).max(1), heads, 0)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        codes = np.nan_to_num(np.abs(c.reshape(n, 4, 128)) / scales[:, :, None]).sum(0)
+    return 2.0 ** -9 / 28 * p.max(1)[:, None] * (V[:, :, None] * codes[None]).reshape(H, 512)
+
+
+def expect(wl, layer_i, t, positions, n=None, nss=None, any_scales=False):
+    """(out, lse, out bound, lse bound) of token t over logical positions, in float64.
+    any_scales: the third bound as small_weight_term has it."""
     v = wl.view(layer_i)
     r = int(dsa.request_of_tokens(wl.cu_q)[t])
     if n is None:
@@ -43,7 +69,11 @@ def expect(wl, layer_i, t, positions, n=None, nss=None):
     p = np.exp(scale * (q @ keys.T) - lse[:, None])
     A = p @ np.abs(c)
     d = 576 * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(keys).T).max(1)
-    tol = 2 * d[:, None] * ((p * (1 - p)) @ np.abs(c)) + U * np.abs(out) + (U + 3 * 2.0 ** -11) * A * 1.01 + 2.0 ** -11.8 * p.max(1)[:, None] * np.abs(c).sum(0)[None]
+    tol = 2 * d[:, None] * ((p * (1 - p)) @ np.abs(c)) + U * np.abs(out) + (U + 3 * 2.0 ** -11) * A * 1.01
+    if any_scales:
+        tol += small_weight_term(p, block_scales(wl, pages, rows), c)
+    else:
+        tol += 2.0 ** -11.8 * p.max(1)[:, None] * np.abs(c).sum(0)[None]
     return out, lse, tol, d + 2.0 ** -20 * (1 + np.abs(lse))
 
 

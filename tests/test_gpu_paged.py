@@ -150,6 +150,21 @@ def test_smallest_and_largest_queries(fmt):
     check_all(fmt, wl, out, lse)
 
 
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("fmt", ["fp8_ds_mla", "e4m3", "bf16"])
+def test_infinities_and_nan_in_a_query_stay_in_their_head(fmt, heads):
+    wl = synth.make_workload(f"paged/inf/{fmt}", [700, 130], [1, 2], heads, latent_format=fmt, layers=(("l", 64, False, None),))
+    q = wl.layers[0].q.reshape(-1, heads, 576)
+    want = [PC.expect(wl, 0, t, np.arange(int(n))) for t, n in enumerate(dsa.visible_lengths(wl.cu_q, wl.ctx_len))]
+    q[:, 1, 7], q[:, 3, 300], q[:, 6, 560], q[:, 10, 0] = 0x7f80, 0x7fc0, 0x7fc0, 0xff80
+    out, lse = paged(wl)
+    bad = [1, 3, 6, 10]
+    assert np.isnan(out[:, bad]).all() and np.isnan(lse[:, bad]).all()
+    good = [h for h in range(heads) if h not in bad]   # (heads share scale exponents: not the same bits as without)
+    for t in range(wl.T):
+        PC.check(f"token {t}", out[t, good], lse[t, good], [x[good] for x in want[t]])
+
+
 def test_rising_logits():
     """Keys that grow along the context: every tile raises the running maximum."""
     wl = synth.make_workload("paged/rise", [1500], [1], 16, latent_format="bf16", layers=(("l", 64, False, None),))
@@ -341,37 +356,97 @@ def test_paged_and_sparse_attention_agree_where_the_selection_is_everything():
         PC.check("blocks", out[t], lse[t], want[t])
 
 
-@pytest.mark.parametrize("spread", [3, 7])
-def test_block_scales_of_different_magnitude(spread):
-    """The four blocks of a row 2^spread apart from their neighbours, and rows scaled by up to
-    2^spread either way.  Besides the bounds above, each term of a weight is off by up to half of
-    E4M3's subnormal step: 2^-9 in all, in units in which the largest p_i sc_ib / 2^eb_b of a key
-    and block is at least 28, 2^eb_b being within a factor 2 below the block's largest scale E_b
-    among the first 128 keys.  An output of block b is then off by at most
-    2^-9 / 28 * max_i,b'(p_i 2 sc_ib' / E_b') * E_b * sum_i |code_ib|."""
-    wl = synth.make_workload(f"paged/spread/{spread}", [300, 1100], [1, 2], 16, layers=(("l", 64, False, None),))
+def _with_scales(name, heads, change, lens=(128 + 64 * 9, 1500)):
+    """A workload whose block scales are change(scales [rows, 4], ids of each request's rows), with
+    so many tokens that a CTA walks a whole token's tiles."""
+    wl = synth.make_workload(f"paged/{name}", list(lens), [70, 80], heads, layers=(("l", 64, False, None),))
     rows = wl.latent.reshape(-1, 656)
     sc = np.ascontiguousarray(rows[:, 512:528]).view("<f4")
-    rng = synth.stream(spread, "paged/spread")
-    row = np.exp2(rng.uniform(-spread, spread, (len(sc), 1)))
-    block = np.exp2(spread * (np.arange(4) - 3.0))
+    ids = [wl.block_table[r, np.arange(n) // 64].astype(np.int64) * 64 + np.arange(n) % 64 for r, n in enumerate(lens)]
     with np.errstate(over="ignore", invalid="ignore"):
-        rows[:, 512:528] = (sc * row * block).astype("<f4").view(np.uint8).reshape(-1, 16)
+        sc = change(sc, ids).astype("<f4")
+    rows[:, 512:528] = sc.view(np.uint8).reshape(-1, 16)
+    return wl, ids
+
+
+def _check_any_scales(name, wl):
     out, lse = paged(PC.spoil_unused(wl))
-    n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
-    for t in range(wl.T):
-        o, l, tol, ltol = PC.expect(wl, 0, t, np.arange(int(n_all[t])))
-        r, n = int(dsa.request_of_tokens(wl.cu_q)[t]), int(n_all[t])
-        pages, rw = F.physical(wl.block_table[r], np.arange(n))
-        c, k_pe = F.latent_rows(wl.latent, pages, rw)
-        s4 = np.ascontiguousarray(wl.latent.reshape(-1, 656)[pages * 64 + rw, 512:528]).view("<f4").astype(np.float64)
-        z = wl.sm_scale * (F.decode_bf16(wl.layers[0].q[t]) @ np.concatenate([c, k_pe], 1).T)
-        p = np.exp(z - l[:, None])
-        E = s4[:128].max(0)
-        unit = (p * (2 * s4 / E).max(1)[None]).max(1)                            # [H]
-        codes = np.abs(c.reshape(n, 4, 128) / s4[:, :, None]).sum(0)             # [4, 128]
-        tol = tol + 2.0 ** -9 / 28 * unit[:, None] * (E[:, None] * codes).reshape(1, 512)
-        PC.check(f"spread {spread} token {t}", out[t], lse[t], (o, l, tol, ltol))
+    for t, n in enumerate(dsa.visible_lengths(wl.cu_q, wl.ctx_len)):
+        if t % 9 and t != wl.T - 1:
+            continue
+        PC.check(f"{name} token {t}", out[t], lse[t], PC.expect(wl, 0, t, np.arange(int(n)), any_scales=True))
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("spread", [3, 7])
+def test_block_scales_of_different_magnitude(spread, heads):
+    """The four blocks of a row 2^spread apart from their neighbours, and rows scaled by up to
+    2^spread either way."""
+    rng = synth.stream(spread, "paged/spread")
+
+    def change(sc, ids):
+        return sc * np.exp2(rng.uniform(-spread, spread, (len(sc), 1))) * np.exp2(spread * (np.arange(4) - 3.0))
+    _check_any_scales(f"spread {spread}", _with_scales(f"spread/{spread}", heads, change, (300, 1100))[0])
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("early", [0.0, 2.0 ** -126, 2.0 ** -30, 2.0 ** -10, 2.0 ** 10])
+def test_one_blocks_scales_change_after_the_first_keys(early, heads):
+    """In a request's first 128 keys one block is zeros, or far below or above what it is later:
+    the other blocks' weights keep their bits."""
+    def change(sc, ids):
+        for r, i in enumerate(ids):
+            sc[i[:128], 2 * r + 1] *= np.float32(early)
+            if early == 2.0 ** -126:
+                sc[i[:128], 2 * r + 1] = np.float32(early)
+        return sc
+    _check_any_scales(f"early {early}", _with_scales(f"early/{heads}", heads, change)[0])
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("at", [0, 5, 300])
+@pytest.mark.parametrize("seen", [True, False])
+def test_one_key_with_a_large_block(seen, at, heads):
+    """One key with a block 2^12 above the others, of ordinary logit (it takes over that block's
+    output, the other blocks keep their bits) or far below (no block may lose any)."""
+    wl, ids = _with_scales(f"large/{heads}", heads, lambda sc, ids: sc)
+    rows = wl.latent.reshape(-1, 656)
+    sc = np.ascontiguousarray(rows[:, 512:528]).view("<f4")
+    pe = np.zeros((len(rows), 64), np.float32)
+    for r, i in enumerate(ids):
+        sc[i[at], 3 * r] *= np.float32(2.0 ** 12)
+        pe[i[at], 0] = 0.0 if seen else -40.0 / wl.sm_scale
+    rows[:, 512:528] = sc.view(np.uint8).reshape(-1, 16)
+    rows[:, 528:] = synth.to_bf16_bits(pe).astype("<u2").view(np.uint8).reshape(-1, 128)
+    q = F.decode_bf16(wl.layers[0].q).astype(np.float32)
+    q[..., 512:] = 0.0
+    q[..., 512] = 1.0
+    for t, r in enumerate(dsa.request_of_tokens(wl.cu_q)):
+        q[t, :, 128 * 3 * r:128 * 3 * r + 128] = 0.0   # the large block does not enter the logits
+    wl.layers[0].q = synth.to_bf16_bits(q)
+    _check_any_scales(f"large {seen} {at}", wl)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("small", [2.0 ** -126, 2.0 ** -24])
+def test_all_scales_grow_after_keys_that_take_the_weight(small, heads):
+    """128 keys of tiny scale that every query prefers, before ordinary ones: the output is the
+    ordinary keys', whose weights are a millionth of the sum, with their bits."""
+    def change(sc, ids):
+        for i in ids:
+            sc[i[:128]] = np.float32(small)
+        return sc
+    wl, ids = _with_scales(f"sink/{heads}", heads, change)
+    rows = wl.latent.reshape(-1, 656)
+    pe = np.zeros((len(rows), 64), np.float32)
+    for i in ids:
+        pe[i[:128], 0] = 14.0 / wl.sm_scale
+    rows[:, 528:] = synth.to_bf16_bits(pe).astype("<u2").view(np.uint8).reshape(-1, 128)
+    q = F.decode_bf16(wl.layers[0].q).astype(np.float32)
+    q[..., 512:] = 0.0
+    q[..., 512] = 1.0
+    wl.layers[0].q = synth.to_bf16_bits(q)
+    _check_any_scales(f"sink {small}", wl)
 
 
 def test_pages_past_four_gigabytes():
