@@ -350,21 +350,33 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 // One CTA per token; warp w owns the row's entries [32 c w, 32 c (w + 1)), c
-// steps of one entry a lane, so that loads are coalesced and a scan over the
-// warps and a ballot a step give every kept entry its place in ascending order.
-// The threshold is the k-th largest key, by up to four rounds of an 8-bit
-// histogram that every warp scans for itself; a round whose digit holds exactly
-// the keys still wanted is the last.  kReg > 0: rows of up to kReg entries a
-// thread, read once into registers; 0: rows of any length, read from L1/L2 in
-// every round.
-constexpr int kTopThreads = 1024;
+// steps of one entry a lane, so that loads are coalesced and a ballot a step
+// gives every kept entry its place in ascending order.
+//
+// The threshold is the k-th largest key.  A bound below it first: of A warps'
+// entries each warp's j-th largest thread maximum, j = ceil(k / A), has at least
+// j A >= k keys at or above the smallest of those.  A histogram of 512 equal
+// steps from there to the largest key leaves a few keys in the threshold's step,
+// and up to three more split that step again; one whose step holds exactly the
+// keys still wanted is the last.  (Histograms of the keys' own 8-bit digits, all
+// keys in the first one and every warp scanning each, took 14.9 us for four rows
+// of 16,375 entries and 5.5 us for 32 of 512 to 1,024, where this takes 8.3 and
+// 4.1 to 4.4.)  What is left is a chain: lengths, loads, the bound, one or two
+// histograms, the places, 0.3 to 0.8 us each.
+// kReg > 0: rows of up to kReg entries a thread, read once into registers (1 where
+// that holds a row: 43.6 us for 2,048 rows of 1,000, 45.8 with 16); 0: rows of
+// any length, read from L1/L2 in every pass (40,000 entries: 36 us).
+constexpr int kTopThreads = 1024, kTopWarps = kTopThreads / 32, kBins = 512, kMaxJ = 8;
 
 template <int kReg>
 __global__ void __launch_bounds__(kTopThreads)
 block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __restrict__ blocks,
                   int32_t* __restrict__ blocks_len) {
-  __shared__ int hist[4][256];   // one per round, so that no round waits to clear another's
-  __shared__ int2 part[kTopThreads / 32];
+  static_assert(kReg < 32, "a bit a step");
+  __shared__ __align__(16) int hist[4][kBins];   // one per round, so that no round waits to clear another's
+  __shared__ uint2 top[kTopWarps];
+  __shared__ int2 part[kTopWarps];
+  __shared__ int4 found;
   ptx::griddep_wait();
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -387,112 +399,147 @@ block_topk_kernel(Batch b, const float* __restrict__ scores, int k, int32_t* __r
   }
   if (take == 0) return;
   const int c = (nb + kTopThreads - 1) / kTopThreads, i0 = warp * c * 32 + lane;
+  const int steps = i0 < nb ? min(c, (nb - i0 + 31) / 32) : 0;   // of this lane
   uint32_t reg[kReg > 0 ? kReg : 1];
   if constexpr (kReg > 0) {
 #pragma unroll
+    for (int u = 0; u < kReg; ++u) reg[u] = u < steps ? __float_as_uint(__ldg(row + i0 + 32 * u)) : 0u;   // all in flight
+#pragma unroll
     for (int u = 0; u < kReg; ++u) {
       if (u >= c) break;
-      reg[u] = i0 + 32 * u < nb ? order_key(__ldg(row + i0 + 32 * u)) : 0u;
+      reg[u] = u < steps ? order_key(__uint_as_float(reg[u])) : 0u;
     }
   }
-  // f(index, key, whether there is one) for every step, by whole warps
+  // f(step, key, whether there is one) for every step, by whole warps
   auto each = [&](auto&& f) {
     if constexpr (kReg > 0) {
 #pragma unroll
       for (int u = 0; u < kReg; ++u) {
         if (u >= c) break;
-        f(i0 + 32 * u, reg[u], i0 + 32 * u < nb);
+        f(u, reg[u], u < steps);
       }
     } else {
-      for (int u = 0; u < c; ++u) {
-        const int i = i0 + 32 * u;
-        f(i, i < nb ? order_key(__ldg(row + i)) : 0u, i < nb);
-      }
+      for (int u = 0; u < c; ++u) f(u, u < steps ? order_key(__ldg(row + i0 + 32 * u)) : 0u, u < steps);
     }
   };
-  static_assert(kTopThreads == 4 * 256, "a thread clears one counter");
-  (&hist[0][0])[tid] = 0;
-  __syncthreads();
-  uint32_t prefix = 0;   // the threshold key's leading bits found so far
-  int need = take;       // keys still wanted among those that share them
+  for (int i = tid; i < 4 * kBins; i += kTopThreads) (&hist[0][0])[i] = 0;
+  uint32_t low = 0, base;
+  {
+    uint32_t mx = 0;   // (an entry that is not there, 0, is below any other and at least a NaN)
+    each([&](int, uint32_t key, bool) { mx = max(mx, key); });
+    const int full = nb / (32 * c);   // warps whose entries are all there
+    const int j = full > 0 ? (take + full - 1) / full : kMaxJ + 1;
+    uint32_t first = __reduce_max_sync(0xffffffffu, mx), at = j <= kMaxJ ? first : 0u;
+    for (int i = 1; i < j && j <= kMaxJ; ++i) {   // (one of equal maxima at a time)
+      const unsigned eq = __ballot_sync(0xffffffffu, mx == at);
+      if (lane == __ffs(eq) - 1) mx = 0;
+      at = __reduce_max_sync(0xffffffffu, mx);
+    }
+    if (lane == 0) top[warp] = make_uint2(first, warp < full || j > kMaxJ ? at : 0xffffffffu);
+    __syncthreads();
+    const uint2 x = top[lane];
+    low = __reduce_min_sync(0xffffffffu, x.y);
+    base = __reduce_max_sync(0xffffffffu, x.x) - low;
+  }
+  int shift = max(0, 32 - __clz(base) - 9);   // base, so far: the largest key less low
+  uint32_t width = 0xffffffffu;               // of the step that holds the threshold, less one
+  base = 0;
+  int need = take;   // keys still wanted among those in [low + base, low + base + width]
+  bool all = false;
 #pragma unroll 1
-  for (int round = 0; round < 4; ++round) {
-    const int shift = 24 - 8 * round;
+  for (int round = 0;; ++round) {
     int* h = hist[round];
     each([&](int, uint32_t key, bool there) {
-      if (!there) return;
-      if (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&h[(key >> shift) & 255], 1);
+      const uint32_t x = key - low - base;
+      if (there && key >= low && x <= width) atomicAdd(&h[x >> shift], 1);
     });
     __syncthreads();
-    // lane l: digits 8 l .. 8 l + 7; above = keys in larger digits
-    int cnt[8], sum = 0;
+    if (warp == 0) {   // lane l: steps 16 l .. 16 l + 15; above = keys in larger steps
+      constexpr int kPer = kBins / 32;
+      int cnt[kPer], sum = 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      cnt[u] = h[8 * lane + u];
-      sum += cnt[u];
-    }
-    int above = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_down_sync(0xffffffffu, above, o);
-      if (lane + o < 32) above += y;
-    }
-    above -= sum;
-    int digit = -1, left = 0, have = 0;
-#pragma unroll
-    for (int u = 7; u >= 0; --u) {
-      if (digit < 0 && above < need && above + cnt[u] >= need) {
-        digit = 8 * lane + u;
-        left = need - above;
-        have = cnt[u];
+      for (int u = 0; u < kPer; u += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(&h[kPer * lane + u]);
+        cnt[u] = x.x;
+        cnt[u + 1] = x.y;
+        cnt[u + 2] = x.z;
+        cnt[u + 3] = x.w;
+        sum += x.x + x.y + x.z + x.w;
       }
-      above += cnt[u];
+      int above = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += y;
+      }
+      above -= sum;
+      if (above < need && above + sum >= need) {
+        int step = -1, left = 0, have = 0;
+#pragma unroll
+        for (int u = kPer - 1; u >= 0; --u) {
+          if (step < 0 && above + cnt[u] >= need) {
+            step = kPer * lane + u;
+            left = need - above;
+            have = cnt[u];
+          }
+          above += cnt[u];
+        }
+        found = make_int4(step, left, have, 0);
+      }
     }
-    const unsigned who = __ballot_sync(0xffffffffu, digit >= 0);
-    const int src = __ffs(who) - 1;
-    digit = __shfl_sync(0xffffffffu, digit, src);
-    need = __shfl_sync(0xffffffffu, left, src);
-    have = __shfl_sync(0xffffffffu, have, src);
-    prefix |= (uint32_t)digit << shift;
-    if (have == need) {   // every key of this digit: the threshold is the digit's smallest key
-      need = INT32_MAX;
-      break;
-    }
+    __syncthreads();
+    const int4 got = found;
+    base += (uint32_t)got.x << shift;
+    width = (1u << shift) - 1;
+    need = got.y;
+    all = got.z == need;   // every key of this step: the threshold is its smallest key
+    if (all || shift == 0) break;
+    shift = max(0, shift - 9);
   }
-  // keep every key above the threshold and the first `need` equal to it (after an
-  // early end: every key at or above it)
-  const bool all = need == INT32_MAX;
-  auto sure_of = [&](uint32_t key, bool there) {
-    return __ballot_sync(0xffffffffu, there && (all ? key >= prefix : key > prefix));
-  };
-  auto tie_of = [&](uint32_t key, bool there) { return __ballot_sync(0xffffffffu, there && !all && key == prefix); };
-  int2 mine = make_int2(0, 0);   // this warp's: kept for sure, equal to the threshold
-  each([&](int, uint32_t key, bool there) {
-    mine.x += __popc(sure_of(key, there));
-    mine.y += __popc(tie_of(key, there));
+  // keep every key above the threshold and the first `need` equal to it (all:
+  // every key at or above it)
+  const uint32_t thr = low + base;
+  const uint32_t surely = all ? thr : thr + 1;   // (no key is 2^32 - 1)
+  int2 mine = make_int2(0, 0);           // this warp's: kept for sure, equal to the threshold
+  uint32_t sure_steps = 0, tie_steps = 0;   // kReg: this lane's steps of either kind
+  each([&](int u, uint32_t key, bool there) {
+    if constexpr (kReg > 0) {
+      if (key >= thr) tie_steps |= 1u << u;
+      if (key >= surely) sure_steps |= 1u << u;
+    } else {
+      mine.x += there && key >= surely;
+      mine.y += there && key >= thr && key < surely;
+    }
   });
+  if constexpr (kReg > 0) {
+    const uint32_t there = (1u << steps) - 1;
+    sure_steps &= there;
+    tie_steps &= there & ~sure_steps;
+    mine = make_int2(__popc(sure_steps), __popc(tie_steps));
+  }
+  mine.x = __reduce_add_sync(0xffffffffu, mine.x);
+  mine.y = __reduce_add_sync(0xffffffffu, mine.y);
   if (lane == 0) part[warp] = mine;
   __syncthreads();
-  const int2 p = part[lane];   // 32 warps
-  int2 upto = p;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto.x, o), y = __shfl_up_sync(0xffffffffu, upto.y, o);
-    if (lane >= o) {
-      upto.x += x;
-      upto.y += y;
-    }
-  }
-  int kept = __shfl_sync(0xffffffffu, upto.x - p.x, warp), ties = __shfl_sync(0xffffffffu, upto.y - p.y, warp);
+  if (mine.x + mine.y == 0) return;   // (no barrier follows)
+  const int2 p = lane < warp ? part[lane] : make_int2(0, 0);
+  int kept = __reduce_add_sync(0xffffffffu, p.x), ties = __reduce_add_sync(0xffffffffu, p.y);
   const unsigned below = (1u << lane) - 1;
-  each([&](int i, uint32_t key, bool there) {   // kept, ties: before this step's entries
-    const unsigned sure = sure_of(key, there), tie = tie_of(key, there);
+  auto place = [&](int u, bool is_sure, bool is_tie) {   // kept, ties: before this step's entries
+    const unsigned sure = __ballot_sync(0xffffffffu, is_sure), tie = __ballot_sync(0xffffffffu, is_tie);
     const int t0 = ties + __popc(tie & below);
-    if ((sure >> lane & 1) || ((tie >> lane & 1) && t0 < need))
-      dst[kept + __popc(sure & below) + (all ? 0 : min(t0, need))] = i;
+    if (is_sure || (is_tie && t0 < need)) dst[kept + __popc(sure & below) + (all ? 0 : min(t0, need))] = i0 + 32 * u;
     kept += __popc(sure);
     ties += __popc(tie);
-  });
+  };
+  if constexpr (kReg > 0) {
+    for (unsigned left = __reduce_or_sync(0xffffffffu, sure_steps | tie_steps); left; left &= left - 1) {
+      const int u = __ffs(left) - 1;
+      place(u, sure_steps >> u & 1, tie_steps >> u & 1);
+    }
+  } else {
+    each([&](int u, uint32_t key, bool there) { place(u, there && key >= surely, there && key >= thr && key < surely); });
+  }
 }
 
 }  // namespace
@@ -536,7 +583,9 @@ cudaError_t launch_block_scores(const sml_problem& p, const uint8_t* iq8, const 
 cudaError_t launch_block_topk(const sml_problem& p, const float* scores, int k, int32_t* blocks, int32_t* blocks_len,
                               int32_t* status, cudaStream_t stream) {
   constexpr int kReg = 16;   // rows of up to 16,384 blocks (a million positions) stay in registers
-  auto kernel = p.max_pages <= kReg * kTopThreads ? block_topk_kernel<kReg> : block_topk_kernel<0>;
+  auto kernel = p.max_pages <= kTopThreads          ? block_topk_kernel<1>
+                : p.max_pages <= kReg * kTopThreads ? block_topk_kernel<kReg>
+                                                    : block_topk_kernel<0>;
   return launch_pdl(kernel, dim3(p.num_tokens), dim3(kTopThreads), 0, stream, 0, batch_of(p, status), scores, k, blocks,
                     blocks_len);
 }

@@ -201,6 +201,40 @@ def test_block_topk_long_rows():
         check_topk(wl, scores, k, blocks, count, wl.ctx_len)
 
 
+@pytest.mark.parametrize("pages", [900, 1024, 1025, 16384, 16385])
+@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "outlier", "tiny", "few", "close", "clustered"])
+def test_block_topk_of_every_distribution(pages, kind):
+    """Rows whose candidates leave the threshold's search nothing to go by, or too much: behind the
+    candidates the row holds larger scores, which do not count."""
+    lens = [64 * pages, 64 * pages - 63, 64 * (pages * 2 // 3) + 1, 40 * 64, 33 * 64 + 1]
+    wl = synth.make_workload(f"btd/{pages}", [64] * 5, [1] * 5, 16)
+    wl.ctx_len = np.array(lens, dtype=np.int32)
+    wl.block_table = np.zeros((5, pages), dtype=np.int32)
+    rng = synth.stream(pages, "btd/" + kind)
+    x = rng.standard_normal((5, pages)).astype(np.float32)
+    if kind == "equal":
+        x[:] = -3.5
+    if kind in ("rising", "falling"):
+        x = np.sort(x, 1)[:, ::1 if kind == "rising" else -1].copy()
+    if kind == "outlier":   # one key far above the others, one far below
+        x[:, 5], x[:, 9] = 3e38, -3e38
+    if kind == "tiny":
+        x *= np.float32(2.0 ** -140)   # subnormal, of either sign, and zeros
+    if kind == "few":
+        x[:, :] = np.nan
+        x[:, 3:pages:pages // 40] = 1.0
+    if kind == "close":     # a few last bits apart
+        x = (np.float32(1.0).view(np.uint32) + rng.integers(0, 40, x.shape).astype(np.uint32)).view(np.float32)
+    if kind == "clustered":   # all of the best next to one another
+        x[:, 20:20 + pages // 8] += 50.0
+    for t, n in enumerate(lens):
+        x[t, (n - 1) // 64:] = np.inf
+    for k in (2, 31, 45, 300, 1000):
+        blocks, count, status = run_topk(wl, x, k)
+        assert status == (sml.SML_OK, 0)
+        check_topk(wl, x, k, blocks, count, np.array(lens))
+
+
 def test_block_topk_given_lengths_and_bad_requests():
     wl = synth.make_workload("bt/vis", [700, 1000, 300], [3, 2, 1], 16)
     scores = synth.stream(0, "bt/vis").standard_normal((6, wl.max_pages), dtype=np.float32)
