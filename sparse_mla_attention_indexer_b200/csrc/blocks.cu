@@ -129,6 +129,12 @@ __device__ __forceinline__ int visible_of(const Batch& b, int t, int* r, bool* b
 // products, fp32 sums in TMEM).  Warps 0-3 gather the keys and reduce D over
 // the heads (thread = block); warp 4 loads queries up to four ahead and issues the
 // MMAs, so the product of the next token overlaps the reduction of the last.
+// 2,048 queries of 511 blocks take 24.4 us for 21 MB (3.3 us) and products that
+// the tensor cores would do in 6 at this shape: 5 us to the first product, then
+// 1.3 us a token with four CTAs on an SM.  No unit is busy (issue 30 %, shared
+// memory's data pipe half, by the weight loads, 16 a token and thread, and the
+// products' operands); without the reduction's arithmetic it takes 19 us.
+// Walking the tokens by registers and shuffles instead of shared memory cost 1 us.
 constexpr int kTileBlocks = 128, kChunk = 64, kEpiThreads = 128, kScoreThreads = kEpiThreads + 32;
 constexpr int kQBufs = 4;
 constexpr int kQueryBytes = SML_INDEX_HEADS * SML_INDEX_DIM;
@@ -177,7 +183,15 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
     S.abort = 0;
     ptx::fence_mbar_init();
   }
+  if (warp == 4) {
+    ptx::tmem_alloc(&S.tmem_base, 128);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
   ptx::griddep_wait();
+  // this CTA holds its tensor memory: a dependent grid cannot starve it
   if (tid == 0) ptx::griddep_launch_dependents();
   bool any = false;
   if (tid < nt) {
@@ -192,17 +206,10 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
     S.fac[tid] = sq * (b.ssmax ? b.s_index * logf((float)max(1, b.ssmax_len ? ssl : n)) : 1.f);
     any = nb > j0;
   }
-  if (!__syncthreads_or(any)) return;   // no token of the CTA has candidates in this tile
-  if (warp == 4) {
-    ptx::tmem_alloc(&S.tmem_base, 128);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
+  const bool work = __syncthreads_or(any);   // some token of the CTA has candidates in this tile
   volatile int* abort = &S.abort;
   const uint32_t T0 = S.tmem_base;
-  if (warp == 4) {
+  if (work && warp == 4) {
     // ---- queries and products; tokens k = 0, 1, ... of those with candidates here ----
     constexpr uint32_t id = ptx::idesc_f16(SML_INDEX_HEADS, 0, 0, 0);
     const uint32_t key0 = ptx::smem_u32(S.key), q0 = ptx::smem_u32(S.q[0]);
@@ -258,10 +265,10 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
     __syncwarp();
     ptx::mbar_wait(&S.drain, 0, nullptr, 100000u);
     __syncwarp();
-  } else {
+  } else if (work) {
     // ---- keys, then the reduction over the heads ----
     const int j = j0 + tid;
-    const uint32_t dst = ptx::smem_u32(S.key) + (tid >> 3) * 1024 + (tid & 7) * 128;
+    const uint32_t key0 = ptx::smem_u32(S.key);
     bool ok = true, there = false;
     float sb = 0.f;
     int k = 0, last = -1;
@@ -276,26 +283,33 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
         const int pg = j < most ? __ldg(b.block_table + (size_t)last * b.max_pages + j) : -1;
         there = pg >= 0 && pg < rows;
         if (j < most && !there) raise_fault(b.status, SML_FAULT_PAGE);
-        const uint8_t* src = block + (size_t)(there ? pg / SML_PAGE_TOKENS : 0) * SML_INDEX_PAGE_BYTES;
-        const int row = there ? pg % SML_PAGE_TOKENS : 0;
-        sb = __ldcg(reinterpret_cast<const float*>(src + SML_PAGE_TOKENS * SML_INDEX_DIM) + row);
+        auto page_of = [&](int pg) { return block + (size_t)(pg / SML_PAGE_TOKENS) * SML_INDEX_PAGE_BYTES; };
+        const int own = there ? pg : 0;
+        sb = __ldcg(reinterpret_cast<const float*>(page_of(own) + SML_PAGE_TOKENS * SML_INDEX_DIM) + own % SML_PAGE_TOKENS);
+        // eight lanes a key, so that a load touches four lines (a thread a key: 32,
+        // and 4 us more before the first product)
         uint4 v[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          v[c] = there ? __ldcg(reinterpret_cast<const uint4*>(src + row * SML_INDEX_DIM) + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 8; ++c) {
+          const int pk = __shfl_sync(0xffffffffu, there ? pg : -1, 4 * c + (lane >> 3));
+          v[c] = pk >= 0 ? __ldcg(reinterpret_cast<const uint4*>(page_of(pk) + pk % SML_PAGE_TOKENS * SML_INDEX_DIM) + (lane & 7))
+                         : make_uint4(0, 0, 0, 0);
+        }
         ok = epi_all(ok);
         if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((c ^ (tid & 7)) << 4)), "r"(v[c].x),
-                       "r"(v[c].y), "r"(v[c].z), "r"(v[c].w)
+        for (int c = 0; c < 8; ++c) {
+          const int row = 32 * warp + 4 * c + (lane >> 3);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(key0 + row * 128 + (((lane & 7) ^ (row & 7)) << 4)),
+                       "r"(v[c].x), "r"(v[c].y), "r"(v[c].z), "r"(v[c].w)
                        : "memory");
+        }
         ptx::fence_proxy_async();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&S.key_full);
       }
       const int acc = k & 1;
-      ok = ok && warp_wait(&S.q_full[k % kQBufs], (k / kQBufs) & 1, abort) && warp_wait(&S.acc_full[acc], (k >> 1) & 1, abort);
+      ok = ok && warp_wait(&S.acc_full[acc], (k >> 1) & 1, abort);
       if (!ok) {
         *abort = 1;
         break;
@@ -320,15 +334,16 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
         s[2] = fmaf(wb.z, fmaxf(__uint_as_float(v1[4 * c + 2]), 0.f), s[2]);
         s[3] = fmaf(wb.w, fmaxf(__uint_as_float(v1[4 * c + 3]), 0.f), s[3]);
       }
-      if (j < S.nb[i])
-        scores[(size_t)(t0 + i) * b.max_pages + j] = there ? ((s[0] + s[1]) + (s[2] + s[3])) * S.fac[i] * sb : NAN;
+      const float sum = (s[0] + s[1]) + (s[2] + s[3]);
       // D and the weights have been read: the arrival lets the next product and
       // TMA overwrite them.  Loads of the weights that are only issued may still
-      // be on their way; the proxy fence puts them before TMA's writes.
+      // be on their way; the proxy fence puts them before TMA's writes.  The
+      // score is stored after it: the fence would wait for that too.
       ptx::fence_proxy_async();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.acc_free[acc]);
+      if (j < S.nb[i]) scores[(size_t)(t0 + i) * b.max_pages + j] = there ? sum * S.fac[i] * sb : NAN;
       ++k;
     }
   }
