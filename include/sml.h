@@ -309,8 +309,11 @@ int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
  * out = 0 and lse = -inf.  What cached rows hold at or past n_t, or before the
  * window, never matters, NaN included.  The products, the row sums and the
  * accumulated outputs are fp32; each softmax weight enters its product with at
- * least 8 significant bits, as a bf16 has.  Positions in a page outside the
- * pool are masked (SML_FAULT_PAGE).
+ * least 8 significant bits, as a bf16 has, or (FP8 pools) within 2^-15 of the
+ * largest of its head (for fp8_ds_mla: times the block's scale, largest of 4
+ * heads, 8 where H > 16) where that is more.  Positions in a page outside the
+ * pool are masked (SML_FAULT_PAGE).  An infinity or NaN in a head's query stays
+ * in that head.
  * Workspace: SML_STAGE_PAGED.  Nothing in it has to survive between calls. */
 int sml_paged_mla_decode(const sml_problem* p, const void* q, sml_cache latent, int32_t window, void* out,
                          float* lse, void* workspace, size_t ws_bytes, void* stream);
@@ -343,7 +346,7 @@ int sml_block_keys_write(sml_cache index_cache, const int32_t* pages, int32_t n,
  * for the blocks j < (n_t - 1) / 64 (integer division) that lie wholly before
  * the block of the token's newest position; kb8_j, sb_j: row
  * block_table[r, j] of block_cache.  iq8, iq_scale, iw as in
- * sml_indexer_scores.  scores [T, max_pages] fp32; other entries are not
+ * sml_indexer_scores, iw 16-B aligned.  scores [T, max_pages] fp32; other entries are not
  * written.  A page outside block_cache scores NaN (which ranks last) and sets
  * SML_FAULT_PAGE (workspace NULL or >= 256 B).  FP8 products are exact; sums
  * accumulate in fp32. */

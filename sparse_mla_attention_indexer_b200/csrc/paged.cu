@@ -637,7 +637,8 @@ __device__ __forceinline__ float log_rel(const float (&sc)[4], const float (&ebf
 // risen (what O holds is that much smaller).  O scales by powers of two, exactly.
 //
 // In: z the logits + lk; out: z less M_h.  last: the tile whose PV O waits for;
-// -1 where O holds nothing yet.
+// -1 where O holds nothing yet.  False: that wait gave up (every warp takes part
+// in the barriers all the same).
 template <int kFmt, int kHU, int kHP>
 __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], float2 (&nM)[kHP], float2 (&lrow)[kHP],
                                        const float (&scv)[4], float (&ebf)[4], float& lk, uint32_t T0, int last) {
@@ -647,6 +648,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, hq = warp >> 2;
   // this thread's latent dim of output block 0, this quarter's heads
   const uint32_t o_addr = T0 + kColO + 2 * kHT * hq + ((uint32_t)(32 * q4) << 16);
+  bool ok = true;
   if constexpr (F::kDs) {
 #pragma unroll
     for (int i = 0; i < kHP; ++i) z[i] = __fadd2_rn(z[i], make_float2(-lk, -lk));
@@ -682,8 +684,8 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       lrow[i] = __fmul2_rn(lrow[i], *reinterpret_cast<const float2*>(&S.fac[warp][2 * i]));
       z[i] = __fadd2_rn(z[i], nM[i]);
     }
-    if (any && last >= 0) {
-      if (!warp_wait(&S.pv_done, last & 1, &S.abort)) return false;   // the last tile's PV accumulates into O
+    if (any && last >= 0) ok = warp_wait(&S.pv_done, last & 1, &S.abort);   // the last tile's PV accumulates into O
+    if (any && last >= 0 && ok) {
       ptx::tc_fence_after();
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
@@ -722,9 +724,10 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       const float now = pow2(-to);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ebf[i] = __shfl_sync(0xffffffffu, now, i);
-      if (last >= 0 && __any_sync(0xffffffffu, to != eb)) {
+      const bool moved = last >= 0 && __any_sync(0xffffffffu, to != eb);
+      if (moved) ok = ok && warp_wait(&S.pv_done, last & 1, &S.abort);
+      if (moved && ok) {
         const float f = pow2(eb - to);
-        if (!warp_wait(&S.pv_done, last & 1, &S.abort)) return false;
         ptx::tc_fence_after();
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
@@ -743,7 +746,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
 #pragma unroll
     for (int i = 0; i < kHP; ++i) z[i] = __fadd2_rn(z[i], make_float2(lk, lk));
   }
-  return true;
+  return ok;
 }
 
 template <int kFmt, int kHU>
