@@ -348,7 +348,8 @@ int sml_block_keys_write(sml_cache index_cache, const int32_t* pages, int32_t n,
  * block_table[r, j] of block_cache.  iq8, iq_scale, iw as in
  * sml_indexer_scores, iw 16-B aligned.  scores [T, max_pages] fp32; other entries are not
  * written.  A page outside block_cache scores NaN (which ranks last) and sets
- * SML_FAULT_PAGE (workspace NULL or >= 256 B).  FP8 products are exact; sums
+ * SML_FAULT_PAGE (workspace NULL or >= 256 B).  A NaN in a block key or a query
+ * gives NaN scores.  FP8 products are exact; sums
  * accumulate in fp32. */
 int sml_block_scores(const sml_problem* p, const void* iq8, const float* iq_scale, const float* iw,
                      sml_cache block_cache, float* scores, void* workspace, void* stream);

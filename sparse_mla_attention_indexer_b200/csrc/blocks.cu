@@ -164,6 +164,13 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
+// ReLU that keeps a NaN, so that a page with a NaN key ranks last.
+__device__ __forceinline__ float relu(uint32_t x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
+  return y;
+}
+
 __global__ void __launch_bounds__(kScoreThreads, 4)
 block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk, const float* __restrict__ iq_scale,
                     const float* __restrict__ iw, const uint8_t* __restrict__ block, long long rows,
@@ -325,14 +332,14 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const float4 wa = w[c], wb = w[8 + c];
-        s[0] = fmaf(wa.x, fmaxf(__uint_as_float(v0[4 * c]), 0.f), s[0]);
-        s[1] = fmaf(wa.y, fmaxf(__uint_as_float(v0[4 * c + 1]), 0.f), s[1]);
-        s[2] = fmaf(wa.z, fmaxf(__uint_as_float(v0[4 * c + 2]), 0.f), s[2]);
-        s[3] = fmaf(wa.w, fmaxf(__uint_as_float(v0[4 * c + 3]), 0.f), s[3]);
-        s[0] = fmaf(wb.x, fmaxf(__uint_as_float(v1[4 * c]), 0.f), s[0]);
-        s[1] = fmaf(wb.y, fmaxf(__uint_as_float(v1[4 * c + 1]), 0.f), s[1]);
-        s[2] = fmaf(wb.z, fmaxf(__uint_as_float(v1[4 * c + 2]), 0.f), s[2]);
-        s[3] = fmaf(wb.w, fmaxf(__uint_as_float(v1[4 * c + 3]), 0.f), s[3]);
+        s[0] = fmaf(wa.x, relu(v0[4 * c]), s[0]);
+        s[1] = fmaf(wa.y, relu(v0[4 * c + 1]), s[1]);
+        s[2] = fmaf(wa.z, relu(v0[4 * c + 2]), s[2]);
+        s[3] = fmaf(wa.w, relu(v0[4 * c + 3]), s[3]);
+        s[0] = fmaf(wb.x, relu(v1[4 * c]), s[0]);
+        s[1] = fmaf(wb.y, relu(v1[4 * c + 1]), s[1]);
+        s[2] = fmaf(wb.z, relu(v1[4 * c + 2]), s[2]);
+        s[3] = fmaf(wb.w, relu(v1[4 * c + 3]), s[3]);
       }
       const float sum = (s[0] + s[1]) + (s[2] + s[3]);
       // D and the weights have been read: the arrival lets the next product and

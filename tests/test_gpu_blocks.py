@@ -131,6 +131,26 @@ def test_block_scores_of_a_long_chunk_are_the_same_every_time():
     check_scores(wl, pool, runs[0].cpu().numpy(), n_all, tokens=list(range(0, wl.T, 41)) + list(range(2880, 2920)))
 
 
+def test_block_scores_keep_nan():
+    """A NaN in a block key's codes or scale gives that block NaN for every token, one in a query
+    every block of that token; the rest is as without."""
+    wl, pool = scored("bs/nan", [1000, 700], [2, 3])
+    code, scale = [int(wl.block_table[0, j]) for j in (3, 7)]
+    pool[code // 64 * F.INDEXER_PAGE_BYTES + code % 64 * 128 + 77] = 0xFF
+    at = scale // 64 * F.INDEXER_PAGE_BYTES + F.INDEXER_KEYS_BYTES + scale % 64 * 4
+    pool[at:at + 4] = np.frombuffer(np.float32(np.nan).tobytes(), dtype=np.uint8)
+    wl.layers[0].iq8[3, 40, 5] = 0x7F
+    got, status = run_scores(wl, pool)
+    assert status == (sml.SML_OK, 0)
+    assert np.isnan(got[:2, [3, 7]]).all()
+    assert np.isnan(got[3, :OB.candidates(699)]).all()
+    n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
+    check_scores(wl, pool, got, n_all, tokens=[2, 4])
+    clean = np.delete(np.arange(OB.candidates(999)), [3, 7])
+    want, _ = run_scores(wl, np.where(pool == 0xFF, 0, pool).astype(np.uint8))
+    assert np.array_equal(got[0, clean], want[0, clean])
+
+
 def test_block_scores_given_lengths_and_bad_pages():
     wl, pool = scored("bs/vis", [700, 1000], [3, 2])
     vis = np.array([0, 65, 700, 64, 513], dtype=np.int32)
