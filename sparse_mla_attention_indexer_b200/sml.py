@@ -201,20 +201,30 @@ def declared_entry_points(header: str = HEADER):
     return sorted(set(re.findall(r"^[A-Za-z_][\w \*]*?\b(sml_\w+)\s*\(", text, flags=re.M)))
 
 
+# A call's arguments take as long as its launch: what follows is kept short.
+
 def _p(x) -> int | None:
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return x   # an address
+
+
+_cuda_ready = False
 
 
 def _s(stream) -> int | None:
     if stream is None:
-        # the current stream's handle without building a Stream object (0.3 against 4 us a call)
-        if not (torch.cuda.is_initialized() or torch.cuda.is_available()):
-            return None
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the current stream's handle without building a Stream object (0.2 against 4 us a call)
+        global _cuda_ready
+        if not _cuda_ready:
+            if not torch.cuda.is_available():
+                return None
+            torch.cuda.init()
+            _cuda_ready = True
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -230,7 +240,7 @@ def _check(code: int):
 
 
 def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def make_problem(*, num_heads, topk, rope_dim, cu_q, ctx_len, block_table, max_ctx=None,
@@ -254,7 +264,7 @@ def cache(pool, page_bytes: int) -> Cache:
     """Cache descriptor of a uint8 pool tensor (or None for an absent cache)."""
     if pool is None:
         return Cache(None, 0, 0, 0.0)
-    return Cache(_p(pool), _nbytes(pool) // page_bytes, 0, 0.0)
+    return Cache(_p(pool), pool.nbytes // page_bytes)   # format 0, no scale
 
 
 def latent_cache(latent) -> Cache:
