@@ -129,12 +129,13 @@ __device__ __forceinline__ int visible_of(const Batch& b, int t, int* r, bool* b
 // products, fp32 sums in TMEM).  Warps 0-3 gather the keys and reduce D over
 // the heads (thread = block); warp 4 loads queries up to four ahead and issues the
 // MMAs, so the product of the next token overlaps the reduction of the last.
-// 2,048 queries of 511 blocks take 24.4 us for 21 MB (3.3 us) and products that
-// the tensor cores would do in 6 at this shape: 5 us to the first product, then
-// 1.3 us a token with four CTAs on an SM.  No unit is busy (issue 30 %, shared
-// memory's data pipe half, by the weight loads, 16 a token and thread, and the
-// products' operands); without the reduction's arithmetic it takes 19 us.
-// Walking the tokens by registers and shuffles instead of shared memory cost 1 us.
+// 2,048 queries of 511 blocks take 24.8 us for 21 MB (3.3 us) and products that
+// the tensor cores would do in 6 at this shape: 8 us before the first product and
+// after the last, then 0.3 us a token and tile on each SM.  Shared memory's pipe
+// is what that takes: the weights (16 loads of 16 B a warp), the products'
+// operands and TMA's queries, about 510 of 560 cycles; without the reduction's
+// arithmetic and weights it is 19 us in all.  Two tiles of blocks to each weight
+// read: 22.3 us here, but 13.4 instead of 11.9 for 512 queries.
 constexpr int kTileBlocks = 128, kChunk = 64, kEpiThreads = 128, kScoreThreads = kEpiThreads + 32;
 constexpr int kQBufs = 4;
 constexpr int kQueryBytes = SML_INDEX_HEADS * SML_INDEX_DIM;
@@ -182,7 +183,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
   if (tid == 0) {
     for (int i = 0; i < kQBufs; ++i) ptx::mbar_init(&S.q_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&S.acc_full[i], 1);
+      ptx::mbar_init(&S.acc_full[i], 2);   // the products' commit, and warp 4's own arrival
       ptx::mbar_init(&S.acc_free[i], 4);
     }
     ptx::mbar_init(&S.key_full, 4);
@@ -262,6 +263,10 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
           ptx::mma_f8(T0 + (k & 1) * SML_INDEX_HEADS, ptx::sdesc_sw128(key0 + 32 * kk),
                       ptx::sdesc_sw128(q0 + (k % kQBufs) * kQueryBytes + 32 * kk), id, kk > 0);
         ptx::mma_commit(&S.acc_full[k & 1]);
+        // This warp has waited for the query and its weights: its arrival passes
+        // them on (a wait of every reducing warp for them costs 1.3 us at 2,048
+        // queries).
+        ptx::mbar_arrive(&S.acc_full[k & 1]);
       }
       __syncwarp();
     }
@@ -279,6 +284,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
     bool ok = true, there = false;
     float sb = 0.f;
     int k = 0, last = -1;
+    // (A wait that gives up still goes on to the next request's barrier, or the end.)
     for (int i = 0; i < nt; ++i) {
       if (S.nb[i] <= j0) continue;
       if (S.req[i] != last) {
@@ -319,7 +325,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap qmap, Batch b, int chunk
       ok = ok && warp_wait(&S.acc_full[acc], (k >> 1) & 1, abort);
       if (!ok) {
         *abort = 1;
-        break;
+        continue;
       }
       ptx::tc_fence_after();
       const uint32_t d = T0 + ((uint32_t)(32 * warp) << 16) + acc * SML_INDEX_HEADS;
