@@ -30,14 +30,15 @@
 //
 // What bounds it, and what it measured (B200, 6.57 TB/s copy):
 //   * 16 heads, 32 contexts of 8K to 64K tokens: HBM.  143 us for 787 MB, 5.5
-//     TB/s; bf16 rows of the same batch 224 us, 94 % of the copy rate.  A tile
+//     TB/s; bf16 rows of the same batch 220 us, 96 % of the copy rate.  A tile
 //     takes 2.0 us against 1.9 of a 148th of that rate; the rest is what stands
 //     before and after the loop (first loads, uneven finish, join).
 //   * 128 heads, 32 tokens of 60,000 (four groups of 32 heads, which read a tile
 //     from L2 after the first): 906 us, 590 TFLOP/s of the attention's own.  The
 //     two buffers' cycle bounds it: load 0.75 us, QK^T 0.6, softmax 1.2, PV 0.5
-//     and the hand-overs between them, 4.6 us for two tiles; no unit is busy (issue
-//     56 %, shared memory's banks 34 %, L2 35 %).  A third buffer does not fit
+//     and the hand-overs between them, 4.4 us for two tiles; no unit is busy (issue
+//     45 %, tensor pipe 30 %, L2 35 %; products' operands, TMA and weights take
+//     about 60 % of shared memory's cycles).  A third buffer does not fit
 //     beside the query and the weights (224 KB), nor 64 heads' O and logits in
 //     TMEM; weights handed to PV in two waves, two loading warps, and raising M_h
 //     further at a time changed nothing.
@@ -175,8 +176,8 @@ struct PlanSmem {
   long long part[32];   // per warp of the block
   int longest[32];
   long long tok0;
-  int t0;
-  Tok tok[32];          // the tokens of a batch of at most 32
+  int t0, base;
+  Tok tok[32];          // tokens base to base + 31: a small batch's, else those from where the range starts
 };
 
 // a / b of non-negative numbers, in 32 bits where both fit (a 64-bit division
@@ -192,8 +193,8 @@ __device__ __forceinline__ int cta_of(long long total, int used, long long u) { 
 // but the longest token decides.  A piece costs about as much as three tiles
 // more (its query, its first tile, its output), and joining split tokens two.
 // 128 heads (37 CTAs a head group), 32 tokens: over 32 selected blocks, selection
-// included, 63 us with whole tokens and 81 with equal ranges; over 60,000 tokens
-// of context 992 and 940.
+// included, 49 us with whole tokens and 60 with equal ranges; over 60,000 tokens
+// of context equal ranges are 5 % faster.
 __device__ __forceinline__ void share(Range& R, int T, int cpg, int gi, int longest) {
   const long long most = div_ll(R.total + cpg - 1, cpg);
   R.m = T <= cpg ? (int)((unsigned)cpg / (unsigned)T) : 0;
@@ -221,20 +222,22 @@ __device__ __forceinline__ int2 holders(const Range& R, int nt) {
   return make_int2(cta_of(R.total, R.used, R.tok0), cta_of(R.total, R.used, R.tok0 + nt - 1));
 }
 
-// Token t's lengths: a small batch's are in shared memory, else they are read again.
+// Token t's lengths, from shared memory where they are there.
 __device__ __forceinline__ Tok token_of(const Params& P, const PlanSmem& S, int t) {
-  return P.T <= 32 ? S.tok[t] : token_at(P, t);
+  const unsigned i = t - S.base;
+  return i < 32 ? S.tok[i] : token_at(P, t);
 }
 
-// Every thread of the block calls it.  Up to 32 tokens: each warp for itself
-// (with the scan over the block below, 2.0 us instead of 1.0 from the first load
-// to the range).
+// Every thread of the block calls it.  Up to 32 tokens: each warp for itself, 1.6
+// us from the first load to the range (1.3 where one warp plans for all, which
+// changed nothing in all; with the scan over the block below, 1 us more).
 __device__ __forceinline__ Range plan_range(const Params& P, int gi, PlanSmem& S) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Range R;
   if (P.T <= 32) {
     const Tok tk = token_at(P, min(lane, P.T - 1));
     if (warp == 0) S.tok[lane] = tk;
+    if (threadIdx.x == 0) S.base = 0;
     const int mine = lane < P.T ? tiles_of(tk) : 0;   // at most 2^23 each
     int upto = mine;
 #pragma unroll
@@ -255,11 +258,13 @@ __device__ __forceinline__ Range plan_range(const Params& P, int gi, PlanSmem& S
     __syncthreads();
     return R;
   }
+  // A thread a token, or a few: their tiles, summed over the block.
   const int per = (P.T + kThreads - 1) / kThreads, a = min(P.T, (int)threadIdx.x * per), b = min(P.T, a + per);
+  const Tok own = token_at(P, min(a, P.T - 1));
   long long mine = 0;
   int longest = 0;
   for (int t = a; t < b; ++t) {
-    const int nt = tiles_of(token_at(P, t));
+    const int nt = tiles_of(t == a ? own : token_at(P, t));
     mine += nt;
     longest = max(longest, nt);
   }
@@ -283,15 +288,11 @@ __device__ __forceinline__ Range plan_range(const Params& P, int gi, PlanSmem& S
     longest = max(longest, S.longest[w]);
   }
   share(R, P.T, P.ws.cpg, gi, longest);
-  if (R.m > 0) {
-    piece(R, gi, tiles_of(token_at(P, min(R.t0, P.T - 1))));
-    return R;
-  }
   const long long first = before + upto - mine;   // first tile of token a
-  if (first <= R.ub && R.ub < first + mine) {
+  if (R.m == 0 && first <= R.ub && R.ub < first + mine) {
     long long at = first;
     for (int t = a; t < b; ++t) {
-      const int nt = tiles_of(token_at(P, t));
+      const int nt = tiles_of(t == a ? own : token_at(P, t));
       if (R.ub < at + nt) {
         S.t0 = t;
         S.tok0 = at;
@@ -301,8 +302,16 @@ __device__ __forceinline__ Range plan_range(const Params& P, int gi, PlanSmem& S
     }
   }
   __syncthreads();
-  R.t0 = S.t0;
-  R.tok0 = S.tok0;
+  if (R.m == 0) {
+    R.t0 = S.t0;
+    R.tok0 = S.tok0;
+  }
+  // The range's own tokens stay in shared memory where a thread holds one each
+  // (a load round less at every token's start).
+  if (threadIdx.x == 0) S.base = per == 1 ? R.t0 : P.T;
+  if (per == 1 && a < b && (unsigned)(a - R.t0) < 32) S.tok[a - R.t0] = own;
+  __syncthreads();
+  if (R.m > 0) piece(R, gi, tiles_of(token_of(P, S, min(R.t0, P.T - 1))));
   return R;
 }
 
@@ -319,7 +328,7 @@ struct Fmt {
   static constexpr int kSets = kDs ? 4 : 1;        // weight sets: one per block scale
   // Logit accumulators: one per block scale, and RoPE's.  Both query terms'
   // columns stand side by side (one MMA of twice the width costs about as much
-  // as one: 46 cycles at N = 32, 55 at 64), except those of the last block
+  // as one: 42 cycles at N = 32, 49 at 64), except those of the last block
   // where 32 heads would leave no room for them beside O: they are summed.
   static constexpr bool split_terms(int heads, int b) { return !kBf && !(kDs && heads == 32 && b == 3); }
   static constexpr uint32_t col_block(int heads, int b) { return kDs ? 2 * heads * b : 0; }
