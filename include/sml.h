@@ -314,7 +314,8 @@ int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
  * heads, 8 where H > 16) where that is more.  Positions in a page outside the
  * pool are masked (SML_FAULT_PAGE).  An infinity or NaN in a head's query stays
  * in that head.
- * Workspace: SML_STAGE_PAGED.  Nothing in it has to survive between calls. */
+ * Workspace: SML_STAGE_PAGED.  Nothing in it has to survive between calls; calls
+ * that may overlap on the GPU need one each. */
 int sml_paged_mla_decode(const sml_problem* p, const void* q, sml_cache latent, int32_t window, void* out,
                          float* lse, void* workspace, size_t ws_bytes, void* stream);
 
