@@ -35,13 +35,15 @@
 //     before and after the loop (first loads, uneven finish, join).
 //   * 128 heads, 32 tokens of 60,000 (four groups of 32 heads, which read a tile
 //     from L2 after the first): 906 us, 590 TFLOP/s of the attention's own.  The
-//     two buffers' cycle bounds it: load 0.75 us, QK^T 0.6, softmax 1.2, PV 0.5
-//     and the hand-overs between them, 4.4 us for two tiles; no unit is busy (issue
-//     45 %, tensor pipe 30 %, L2 35 %; products' operands, TMA and weights take
-//     about 60 % of shared memory's cycles).  A third buffer does not fit
-//     beside the query and the weights (224 KB), nor 64 heads' O and logits in
-//     TMEM; weights handed to PV in two waves, two loading warps, and raising M_h
-//     further at a time changed nothing.
+//     two buffers' cycle bounds it, and shared memory under it: of 3,500 to 3,900
+//     cycles a tile the products' operands take 1,930 (a product costs its
+//     operands' bytes / 128 B, 52 cycles at N = 64 whatever their majors), TMA's
+//     writes 660 and the weights 400, and each slows the others (PV takes 2,900
+//     cycles from its first product to its last).  Issue 45 %, L2 35 %.  Twice the
+//     heads a product would read the tile half as often, but 64 heads' O and
+//     logits do not fit in TMEM, nor a third buffer beside the query and the
+//     weights (224 KB); weights handed to PV in two waves, two loading warps, and
+//     raising M_h further at a time changed nothing.
 //   * few tiles a CTA (selected blocks, one short context): the chain of first
 //     loads, first tile, output and join, 14 us at least.  Code that a CTA runs
 //     once or twice costs what it takes to fetch, 0.5 to 0.9 us for 2 to 3 KB of
