@@ -309,9 +309,12 @@ int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
  * out = 0 and lse = -inf.  What cached rows hold at or past n_t, or before the
  * window, never matters, NaN included.  The products, the row sums and the
  * accumulated outputs are fp32; each softmax weight enters its product with at
- * least 8 significant bits, as a bf16 has, or (FP8 pools) within 2^-15 of the
+ * least 8 significant bits, as a bf16 has, or (FP8 pools) within 2^-18 of the
  * largest of its head (for fp8_ds_mla: times the block's scale, largest of 4
- * heads, 8 where H > 16) where that is more.  Positions in a page outside the
+ * heads, 8 where H > 16) where that is more.  Which way a small weight is
+ * rounded differs from row to row of a tile, so that the tens of thousands
+ * behind a dominant key keep their sum: n of them are off by some 2^-20 sqrt(n)
+ * of the largest together.  Positions in a page outside the
  * pool are masked (SML_FAULT_PAGE).  An infinity or NaN in a head's query stays
  * in that head.
  * Workspace: SML_STAGE_PAGED.  Nothing in it has to survive between calls; calls

@@ -22,7 +22,7 @@
 //     scale, RoPE apart in bf16;
 //   * warps 0-15 read S^T (thread = key x a quarter of the heads), scale, take
 //     2^(z - M_h) and write the weights, block scale folded in, as two E4M3
-//     terms (bf16 pools: two bf16 terms);
+//     terms, the second times 2^4 (bf16 pools: two bf16 terms);
 //   * warp 17 issues O^T += C^T W^T, the tile read MN-major, and frees the tile a
 //     quarter of the dims at a time.
 // The latent is never converted, and every wait is bounded: one that gives up
@@ -455,18 +455,29 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float& x0, float& x1) {
   x1 -= r.y;
   return c;
 }
-// Two weights (at most 448) in half precision as two E4M3 terms, hi + lo: eight
-// significant bits, as many as a bf16 has.  x - hi is exact in half precision.
-// Below E4M3's smallest normal value 2^-6 a term is off by at most half a
-// subnormal step, 2^-10.  (hi without the conversion back, by Veltkamp's
+// Two weights (at most 448) in half precision as two E4M3 terms, hi + 2^-4 lo:
+// eight significant bits, as many as a bf16 has.  x - hi is exact in half
+// precision and at most 16, so lo stays within 256; the epilogue gives lo's
+// columns of O their 2^-4.  (hi without the conversion back, by Veltkamp's
 // splitting in half precision, measured the same.)
+//
+// Weights below 2^-6 keep lo's subnormal step, 2^-13, and a long context behind a
+// dominant key holds tens of thousands of them, which add up: alike, they would
+// all be rounded the same way, or to nothing.  So lo is rounded with a dither, an
+// offset of less than half a step that depends on the key's row of the tile
+// (dither_of): 128 weights alike are off by at most half a step in all, others at
+// random, and one that is a tenth of a step is a step at a tenth of the rows.
 __device__ __forceinline__ uint32_t half2_to_e4m3x2(__half2 x) {
   return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
 }
-__device__ __forceinline__ void split2_e4m3x2(__half2 x, uint32_t& hi, uint32_t& lo) {
+constexpr float kLoScale = 16.f;
+__device__ __forceinline__ __half2 dither_of(int row) {   // (2 bitrev(row) - 127) / 256 of lo's step 2^-9
+  return __float2half2_rn((float)(2 * (int)(__brev((uint32_t)row) >> 25) - 127) * 0x1p-17f);
+}
+__device__ __forceinline__ void split2_e4m3x2(__half2 x, __half2 dither, uint32_t& hi, uint32_t& lo) {
   hi = half2_to_e4m3x2(x);
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
-  lo = half2_to_e4m3x2(__hsub2_rn(x, *reinterpret_cast<const __half2*>(&h)));
+  lo = half2_to_e4m3x2(__hfma2(__hsub2_rn(x, *reinterpret_cast<const __half2*>(&h)), __float2half2_rn(kLoScale), dither));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -1027,6 +1038,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
     // quarter: this thread owns key (or dim) `row` for heads kHT hq ..
     const int q4 = warp & 3, hq = warp >> 2, row = 32 * q4 + lane, tid = threadIdx.x;
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+    const __half2 dither = dither_of(row);
     auto stage = [&](const Seg& s) {
       stage_query<kFmt, kHU>(P, S, s.t, g, tid);
       ptx::fence_proxy_async();
@@ -1222,8 +1234,8 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
 #pragma unroll
             for (int i = 0; i < kHT / 4; ++i) {
               uint32_t h01, l01, h23, l23;
-              split2_e4m3x2(F::kDs ? __hmul2_rn(p2[2 * i], sc2) : p2[2 * i], h01, l01);
-              split2_e4m3x2(F::kDs ? __hmul2_rn(p2[2 * i + 1], sc2) : p2[2 * i + 1], h23, l23);
+              split2_e4m3x2(F::kDs ? __hmul2_rn(p2[2 * i], sc2) : p2[2 * i], dither, h01, l01);
+              split2_e4m3x2(F::kDs ? __hmul2_rn(p2[2 * i + 1], sc2) : p2[2 * i + 1], dither, h23, l23);
               hi[i] = h01 | (h23 << 16);
               lo[i] = l01 | (l23 << 16);
             }
@@ -1310,7 +1322,7 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         const float back = 1.f / (b == 0 ? ebf[0] : b == 1 ? ebf[1] : b == 2 ? ebf[2] : ebf[3]);   // a power of two
 #pragma unroll
         for (int h = 0; h < kHT; ++h) {
-          const float o = (__uint_as_float(ov[h]) + __uint_as_float(ov[kHT + h])) * osc[h] * back;
+          const float o = fmaf(__uint_as_float(ov[kHT + h]), F::kBf ? 1.f : 1.f / kLoScale, __uint_as_float(ov[h])) * osc[h] * back;
           if (s.whole) {
             const __nv_bfloat16 r = __float2bfloat16_rn(o);
             P.out[(orow + kHT * hq + h) * SML_LATENT_DIM + dim] = *reinterpret_cast<const uint16_t*>(&r);

@@ -1,0 +1,179 @@
+"""The softmax weights of the FP8 pools' attention: many small ones behind a dominant key, on
+the GPU against the float64 oracle.
+
+The logits come through the RoPE key alone (the query's latent dims are 0), so that they do not
+depend on the latents, which have a common offset: weights that are lost do not average out.
+
+Bounds, from the arithmetic that include/sml.h promises (u = 2^-8, half a bf16 step):
+
+* the output's rounding u |out|; each weight of 8 significant bits, three roundings to half
+  precision on the way: (u + 3 * 2^-11) A, A = sum_i p_i |c_i|;
+* the small weights together, whatever the number of keys: 1/224 of the row sum, as mass put on a
+  tile's mean |c|, the largest over the context (tiles are 128 positions from the first page on,
+  however the context is cut).  It stands for a sum of random roundings, at most 2^-14 each in units
+  of which the largest weight is 56 or more: six deviations of 64,000 of them are 6 * 253 * 2^-14 / 56
+  = 1/600, and weights alike, 500 tiles of half a step 2^-14 each, 1/1,800.  fp8_ds_mla: in units of
+  the block's scale exponent, at most 4 of its largest scale (a weight of at most 224 sets it to lie
+  above 56);
+* the logits' sums: as in tests/paged_cases.py.  The log-sum-exp: those, the weights' own sum in fp32
+  (n / 128 terms in a thread, 2^-24 each) and 2^-20 (1 + |lse|) for log2 and exp2.
+"""
+import functools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import dsa, formats as F
+from sparse_mla_attention_indexer_b200 import sml, synth
+from sparse_mla_attention_indexer_b200.device import DeviceWorkload
+from tests import paged_cases as PC, parity
+
+pytestmark = pytest.mark.gpu
+
+ROW = {"fp8_ds_mla": 656, "e4m3": 576, "bf16": 1152}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from sparse_mla_attention_indexer_b200 import build
+    build.build()
+    sml.lib()
+
+
+def put_rows(wl, at, c, k_pe):
+    """Pool rows `at` with latents c [n, 512] and RoPE keys k_pe [n, 64], quantised as the pool is."""
+    rows = wl.latent.reshape(-1, ROW[wl.latent_format])
+    if wl.latent_format == "fp8_ds_mla":
+        codes, scale = synth.quantise_rows(c.astype(np.float32), 128)
+        rows[at, :512] = codes
+        rows[at, 512:528] = scale.astype("<f4").view(np.uint8).reshape(-1, 16)
+        rows[at, 528:] = synth.to_bf16_bits(k_pe.astype(np.float32)).astype("<u2").view(np.uint8).reshape(-1, 128)
+    elif wl.latent_format == "e4m3":
+        rows[at] = synth.to_e4m3(np.concatenate([c, k_pe], 1).astype(np.float32) / np.float32(synth.PLAIN_SCALE))
+    else:
+        x = np.concatenate([c, k_pe], 1).astype(np.float32)
+        rows[at] = synth.to_bf16_bits(x).astype("<u2").view(np.uint8).reshape(-1, 1152)
+
+
+def rows_of(wl, r, positions):
+    return wl.block_table[r, positions // 64].astype(np.int64) * 64 + positions % 64
+
+
+@functools.lru_cache(maxsize=2)
+def latents(n, seed=0):
+    return synth.stream(seed, f"weights/latents/{n}").normal(1.0, 1.0, (n, 512)).astype(np.float32)
+
+
+def sink_case(fmt, heads, n, new, sigma, at=0):
+    """One request of n tokens, `new` of them queries: key `at` holds a share of the softmax that
+    differs by head (0.5, 0.65 and 0.8 of it, every fourth head none above the others), the other
+    keys are alike (sigma = 0) or spread with that deviation."""
+    wl = synth.make_workload(f"weights/{fmt}/{heads}/{new}", [n], [new], heads, latent_format=fmt,
+                             layers=(("l", 64, False, None),))
+    rng = synth.stream(1, f"weights/{fmt}/{n}/{sigma}")
+    pe = np.zeros((n, 64))
+    pe[:, 32:] = rng.standard_normal((n, 32)) if sigma else 0.0
+    pe[at] = 0.0
+    pe[at, :32] = 1.0
+    put_rows(wl, rows_of(wl, 0, np.arange(n)), latents(n), pe)
+    share = np.array([0.5, 0.65, 0.8, 0.0])[np.arange(heads) % 4]
+    z = np.maximum(np.log(n * np.exp(sigma ** 2 / 2) * np.maximum(share, 1e-9) / (1 - share)), 0.0)
+    wl.sm_scale = float(np.float32(1 / 32.0))
+    q = np.zeros((new, heads, 576), np.float32)
+    q[:, :, 512:544] = z[None, :, None]                       # 32 dims of 1 times 1 / 32
+    q[:, :, 544:] = sigma * 32.0 / 32 ** 0.5
+    wl.layers[0].q = synth.to_bf16_bits(q)
+    return wl
+
+
+def tile_mean(x):
+    """Largest mean over tiles of 128 rows of x [n, d]."""
+    pad = np.pad(x, ((0, -len(x) % 128), (0, 0)))
+    return pad.reshape(-1, 128, x.shape[1]).mean(1).max(0)
+
+
+def check_token(name, wl, out, lse, t, n, c, k_pe, scales):
+    q = F.decode_bf16(wl.layers[0].q[t])
+    keys = np.concatenate([c[:n], k_pe[:n]], 1)
+    z = wl.sm_scale * (q[:, 512:] @ k_pe[:n].T)
+    top = z.max(1, keepdims=True)
+    p = np.exp(z - top)
+    l = p.sum(1, keepdims=True)
+    p /= l
+    want, want_lse = p @ c[:n], (top + np.log(l))[:, 0]
+    A = p @ np.abs(c[:n])
+    d = 576 * 2.0 ** -23 * wl.sm_scale * (np.abs(q) @ np.abs(keys).T).max(1)
+    tol = 2 * d[:, None] * ((p * (1 - p)) @ np.abs(c[:n])) + PC.U * np.abs(want) + (PC.U + 3 * 2.0 ** -11) * A * 1.01
+    if wl.latent_format == "fp8_ds_mla":
+        codes = np.abs(c[:n].reshape(n, 4, 128)) / scales[:n, :, None]
+        tol += 4 / 224 * (scales[:n].max(0)[:, None] * tile_mean(codes.reshape(n, 512)).reshape(4, 128)).reshape(1, 512)
+    elif wl.latent_format == "e4m3":
+        tol += tile_mean(np.abs(c[:n]))[None] / 224
+    ltol = d + (n / 128 + 8) * 2.0 ** -24 + 2.0 ** -20 * (1 + np.abs(want_lse))
+    PC.check(f"{name} token {t} (n {n})", out[t], lse[t], (want, want_lse, tol, ltol))
+
+
+def run(wl, window=0):
+    dw = DeviceWorkload(wl)
+    p = dw.problem(0)
+    out = torch.full((wl.T, wl.num_heads, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((wl.T, wl.num_heads), float("nan"), device="cuda")
+    ws = torch.empty(sml.sml_workspace_size(p, sml.SML_STAGE_PAGED), dtype=torch.uint8, device="cuda")
+    sml.sml_workspace_init(ws)
+    sml.sml_paged_mla_decode(p, dw.layers[0].q, dw.latent, out, lse, ws, window=window)
+    assert sml.sml_read_device_status(ws) == (sml.SML_OK, 0)
+    return out.float().cpu().numpy(), lse.cpu().numpy()
+
+
+def check_tokens(name, wl, out, lse, tokens):
+    n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
+    pos = np.arange(int(wl.ctx_len[0]))
+    pages, rows = F.physical(wl.block_table[0], pos)
+    c, k_pe = F.latent_rows(parity.oracle_latent(wl), pages, rows)
+    scales = PC.block_scales(wl, pages, rows) if wl.latent_format == "fp8_ds_mla" else None
+    for t in tokens:
+        check_token(name, wl, out, lse, t, int(n_all[t]), c, k_pe, scales)
+
+
+# More tokens than CTAs a head group (148, or 37 of 128 heads): the first and the last token are one
+# piece; 32: pieces of some 14,000 and 56,000 keys; 1: every CTA a piece.
+@pytest.mark.parametrize("sigma", [0.0, 0.5])
+@pytest.mark.parametrize("n,new", [(64000, 150), (64000, 32), (20000, 150), (41000, 1)])
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("fmt", ["fp8_ds_mla", "e4m3"])
+def test_a_dominant_key_before_a_long_tail(fmt, heads, n, new, sigma):
+    new = new if heads == 16 or new < 100 else 38
+    wl = sink_case(fmt, heads, n, new, sigma)
+    out, lse = run(wl)
+    check_tokens(f"{fmt} {heads} heads sigma {sigma}", wl, out, lse, sorted({0, new // 2, new - 1}))
+
+
+@pytest.mark.parametrize("sigma", [1.0, 3.0])
+@pytest.mark.parametrize("at", [0, 9000, 39990])
+@pytest.mark.parametrize("fmt", ["fp8_ds_mla", "e4m3", "bf16"])
+def test_a_dominant_key_anywhere_among_spread_ones(fmt, at, sigma):
+    """Weights over many binades, the dominant key first, in the middle (the exponent falls, rises and
+    falls again) and near the end."""
+    wl = sink_case(fmt, 16, 40000, 150, sigma, at=at)
+    out, lse = run(wl)
+    check_tokens(f"{fmt} sigma {sigma} at {at}", wl, out, lse, [0, 149])
+
+
+@pytest.mark.parametrize("fmt", ["fp8_ds_mla", "e4m3"])
+def test_several_dominant_keys_and_steps_between_levels(fmt):
+    """Stretches of keys 0, 6, 13, 30 and 60 octaves below the largest, in a mixed order, so that the
+    exponent steps both ways and reaches the depth where it stops following."""
+    n, new = 30000, 150
+    wl = sink_case(fmt, 16, n, new, 0.0)
+    pe = np.zeros((n, 64))
+    levels = np.array([13, 30, 6, 60, 13, 6, 0, 6, 30, 60, 13, 6], np.float64)
+    step = levels[np.arange(n) * len(levels) // n]
+    pe[:, 0] = -step * np.log(2.0) / 8
+    pe[::1777, 0] = 0.0
+    put_rows(wl, rows_of(wl, 0, np.arange(n)), latents(n), pe)
+    q = np.zeros((new, 16, 576), np.float32)
+    q[:, :, 512] = 8.0 * 32 * np.linspace(0.25, 1, 16)[None]
+    wl.layers[0].q = synth.to_bf16_bits(q)
+    out, lse = run(wl)
+    check_tokens(f"{fmt} levels", wl, out, lse, [0, 75, 149])
