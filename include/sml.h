@@ -310,8 +310,9 @@ int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
  * window, never matters, NaN included.  The products, the row sums and the
  * accumulated outputs are fp32; each softmax weight enters its product with at
  * least 8 significant bits, as a bf16 has, or (FP8 pools) within 2^-18 of the
- * largest of its head (for fp8_ds_mla: times the block's scale, largest of 4
- * heads, 8 where H > 16) where that is more.  Which way a small weight is
+ * largest of its head where that is more; fp8_ds_mla: within 2^-14, of weight
+ * over its head's largest times the block's scale, the largest of 4 heads (8
+ * where H > 16) that share an exponent.  Which way a small weight is
  * rounded differs from row to row of a tile, so that the tens of thousands
  * behind a dominant key keep their sum: n of them are off by some 2^-20 sqrt(n)
  * of the largest together.  Positions in a page outside the

@@ -361,6 +361,8 @@ struct __align__(1024) Smem {
   float sc[F::kDs ? F::kBufs : 1][kKT][4];        // [buffer][key] block scales
   __align__(8) float xmax[4][4][kHU / 4];                      // [head quarter][key quarter][head]
   __align__(16) float xscale[4][4][4];            // [head quarter][key quarter][block]
+  float ebtop[16][4];                             // [warp][block] and risen [warp]: see rebase
+  int risen[16];
   __align__(8) float nm[16][kHU / 4], fac[16][kHU / 4];   // [warp][head] -M_h, and what O scales by
   __align__(8) float xsum[4][4][kHU / 4];
   float qs[kHU];                                  // power-of-two query scale per head
@@ -654,9 +656,13 @@ __device__ __forceinline__ float log_rel(const float (&sc)[4], const float (&ebf
 // A head whose largest softmax weight of the tile is above 2^limit takes the
 // integer M_h that puts it in (56, 112]: headroom of 4 for later tiles, and the
 // dominant weights keep all eight bits.  Then the same for each block's weight
-// times scale, over the quarter's heads: the first tile sets eb, one that passes
-// the cap all the same raises it, and it may fall by as much as every M_h has
-// risen (what O holds is that much smaller).  O scales by powers of two, exactly.
+// times scale, over the quarter's heads: eb rises where a product passes the cap,
+// and else, once every M_h has risen by two octaves (`risen`, since the last time),
+// falls to what this tile's largest product needs, so that scales that fall while
+// M_h rises keep their bits.  (Each time at all: 1 to 4 % more in the verification
+// step.)  What O holds grows as eb falls: within kFall octaves of the largest eb so
+// far (ebtop, less what every M_h has risen by since) O stays below 2^112, 2^30 keys
+// of 440 x 448 each.  O scales by powers of two, exactly.
 //
 // In: z the logits + lk; out: z less M_h.  last: the tile whose PV O waits for;
 // -1 where O holds nothing yet.  False: that wait gave up (every warp takes part
@@ -666,6 +672,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
                                        const float (&scv)[4], float (&ebf)[4], float& lk, uint32_t T0, int last) {
   using F = Fmt<kFmt>;
   constexpr int kHT = kHU / 4, kFirst = 1000;
+  constexpr float kFall = 64.f;
   constexpr float kLimit = F::kDs ? kHead<kFmt> + 1.f : kCap<kFmt>;   // (the block's scale may come on top)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, hq = warp >> 2;
   // this thread's latent dim of output block 0, this quarter's heads
@@ -697,7 +704,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       S.nm[warp][h] = neg;
       S.fac[warp][h] = was ? pow2(-by) : 1.f;
     }
-    rise = __reduce_min_sync(0xffffffffu, was ? by : kFirst);
+    rise = __reduce_min_sync(0xffffffffu, was && neg > -INFINITY ? by : kFirst);   // (an infinite M_h: a head of NaN)
     const bool any = __any_sync(0xffffffffu, was && by > 0);   // (also makes the stores visible to the warp)
     __syncwarp();
 #pragma unroll
@@ -729,7 +736,8 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
     float u = -kFar;
 #pragma unroll
     for (int i = 0; i < kHP; ++i) u = fmaxf(u, fmaxf(z[i].x, z[i].y));
-    if (rise >= 4 || group_any(hq, u + lk > kCap<kFmt>)) {
+    int risen = rise == kFirst ? kFirst : S.risen[warp] + rise;
+    if (risen >= 2 || group_any(hq, u + lk > kCap<kFmt>)) {
       float v[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) v[b] = ptx::warp_max_f32(u + lg2(scv[b]));
@@ -740,9 +748,14 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       const float was = b & 2 ? (b & 1 ? ebf[3] : ebf[2]) : (b & 1 ? ebf[1] : ebf[0]);
       const int eb = 127 - (int)(__float_as_uint(was) >> 23);
       const int fit = (int)ceilf(fminf(fmaxf(t - kHead<kFmt>, -126.f), 126.f));
+      const float top = S.ebtop[warp][b] - (float)risen;
       const int to = rise == kFirst               ? fit
                      : t - (float)eb > kCap<kFmt> ? max(fit, eb)
-                                                  : max(min(fit, eb), eb - min(rise, 64));
+                     : t > -INFINITY              ? max(min(fit, eb), (int)(top - kFall))
+                                                  : eb;   // (scales of 0: nothing to fit)
+      risen = 0;
+      __syncwarp();   // every lane has read the old one
+      if (lane < 4) S.ebtop[warp][b] = rise == kFirst ? (float)to : fmaxf(top, (float)to);
       const float now = pow2(-to);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ebf[i] = __shfl_sync(0xffffffffu, now, i);
@@ -765,6 +778,8 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       }
       lk = log_rel(scv, ebf);
     }
+    __syncwarp();
+    if (lane == 0) S.risen[warp] = risen;
 #pragma unroll
     for (int i = 0; i < kHP; ++i) z[i] = __fadd2_rn(z[i], make_float2(lk, lk));
   }

@@ -153,8 +153,7 @@ def test_a_dominant_key_before_a_long_tail(fmt, heads, n, new, sigma):
 @pytest.mark.parametrize("at", [0, 9000, 39990])
 @pytest.mark.parametrize("fmt", ["fp8_ds_mla", "e4m3", "bf16"])
 def test_a_dominant_key_anywhere_among_spread_ones(fmt, at, sigma):
-    """Weights over many binades, the dominant key first, in the middle (the exponent falls, rises and
-    falls again) and near the end."""
+    """Weights over many binades, the dominant key first, in the middle and near the end."""
     wl = sink_case(fmt, 16, 40000, 150, sigma, at=at)
     out, lse = run(wl)
     check_tokens(f"{fmt} sigma {sigma} at {at}", wl, out, lse, [0, 149])
@@ -162,8 +161,8 @@ def test_a_dominant_key_anywhere_among_spread_ones(fmt, at, sigma):
 
 @pytest.mark.parametrize("fmt", ["fp8_ds_mla", "e4m3"])
 def test_several_dominant_keys_and_steps_between_levels(fmt):
-    """Stretches of keys 0, 6, 13, 30 and 60 octaves below the largest, in a mixed order, so that the
-    exponent steps both ways and reaches the depth where it stops following."""
+    """Stretches of keys 0, 6, 13, 30 and 60 octaves below the largest, in a mixed order, with
+    a key at the top of every 1,777."""
     n, new = 30000, 150
     wl = sink_case(fmt, 16, n, new, 0.0)
     pe = np.zeros((n, 64))
@@ -177,3 +176,73 @@ def test_several_dominant_keys_and_steps_between_levels(fmt):
     wl.layers[0].q = synth.to_bf16_bits(q)
     out, lse = run(wl)
     check_tokens(f"{fmt} levels", wl, out, lse, [0, 75, 149])
+
+
+def check_block_scales(name, wl, out, lse, tokens):
+    """Against the contract for fp8_ds_mla, at half of what it allows: a weight within 2^-15 of V_b = the
+    largest p_hi / pmax_h sc_ib of the heads that share an exponent (4, or 8 of 32 heads and more) over
+    all keys, times its head's pmax_h and its code, and the other terms of the module's bounds."""
+    n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
+    pages, rows = F.physical(wl.block_table[0], np.arange(int(wl.ctx_len[0])))
+    c_all, pe_all = F.latent_rows(wl.latent, pages, rows)
+    sc_all = PC.block_scales(wl, pages, rows)
+    for t in tokens:
+        n = int(n_all[t])
+        c, pe, sc = c_all[:n], pe_all[:n], sc_all[:n]
+        q = F.decode_bf16(wl.layers[0].q[t])
+        z = wl.sm_scale * (q[:, 512:] @ pe.T)
+        top = z.max(1, keepdims=True)
+        e = np.exp(z - top)                                      # p / pmax
+        p = e / e.sum(1, keepdims=True)
+        want, want_lse = p @ c, (top + np.log(e.sum(1, keepdims=True)))[:, 0]
+        share = 4 if wl.num_heads == 16 else 8
+        V = np.repeat((e[:, :, None] * sc[None]).max(1).reshape(-1, share, 4).max(1), share, 0)   # [H, 4]
+        codes = np.abs(c.reshape(n, 4, 128) / sc[:, :, None]).sum(0)                            # [4, 128]
+        d = 576 * 2.0 ** -23 * wl.sm_scale * (np.abs(q[:, 512:]) @ np.abs(pe).T).max(1)
+        A = p @ np.abs(c)
+        tol = 2 * d[:, None] * ((p * (1 - p)) @ np.abs(c)) + PC.U * np.abs(want) + (PC.U + 3 * 2.0 ** -11) * A * 1.01
+        tol += (2.0 ** -15 * p.max(1)[:, None, None] * V[:, :, None] * codes[None]).reshape(-1, 512)
+        ltol = d + (n / 128 + 8) * 2.0 ** -24 + 2.0 ** -20 * (1 + np.abs(want_lse))
+        PC.check(f"{name} token {t}", out[t], lse[t], (want, want_lse, tol, ltol))
+
+
+def rising_case(heads, octaves, who, fall, gradual):
+    """160 queries of one request of 2,208 tokens (16 tiles and more in a piece); the logits of the heads
+    `who` rise by `octaves` a tile, the others' are level; from the fifth tile on, block 1's scales are
+    2^-fall of what they were (gradual: reached over ten tiles)."""
+    n, new = 2048 + 160, 160
+    wl = synth.make_workload(f"weights/rise/{heads}", [n], [new], heads, layers=(("l", 64, False, None),))
+    tile = np.arange(n) // 128
+    pe = np.zeros((n, 64))
+    pe[:, :8] = tile[:, None] / 16
+    put_rows(wl, rows_of(wl, 0, np.arange(n)), latents(n), pe)
+    rows = wl.latent.reshape(-1, 656)
+    at = rows_of(wl, 0, np.arange(n))
+    sc = np.ascontiguousarray(rows[at, 512:528]).view("<f4")
+    sc[:, 1] *= np.exp2(-fall * (np.clip((tile - 3) / 10, 0, 1) if gradual else tile >= 4)).astype(np.float32)
+    rows[at, 512:528] = sc.view(np.uint8)
+    q = np.zeros((new, heads, 576), np.float32)
+    q[:, who, 512:520] = octaves                                  # 8 dims, 1/16 a tile, times 2 ln 2
+    wl.layers[0].q = synth.to_bf16_bits(q)
+    wl.sm_scale = float(np.float32(2 * np.log(2.0)))
+    return wl
+
+
+@pytest.mark.parametrize("gradual", [False, True])
+@pytest.mark.parametrize("fall", [8, 16, 40])
+@pytest.mark.parametrize("octaves", [2, 3, 8])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_logits_rise_while_one_blocks_scales_fall(heads, octaves, fall, gradual):
+    """The exponent of a block's weights follows its scales down however slowly every M_h rises."""
+    wl = rising_case(heads, octaves, slice(None), fall, gradual)
+    out, lse = run(wl)
+    check_block_scales(f"octaves {octaves} fall {fall}", wl, out, lse, [0, 80, 159])
+
+
+@pytest.mark.parametrize("fall", [8, 16, 40])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_one_head_rises_while_one_blocks_scales_fall(heads, fall):
+    """One head of every four rises by 3 octaves a tile and does not take the others' bits, nor they its."""
+    wl = rising_case(heads, 3, slice(1, None, 4), fall, False)
+    out, lse = run(wl)
+    check_block_scales(f"one head, fall {fall}", wl, out, lse, [0, 80, 159])
