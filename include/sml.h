@@ -223,12 +223,12 @@ int sml_topk(const sml_problem* p, const float* scores, int32_t* idx, int32_t* i
  *   out      [T, H, 512] fp32;  lse [T, H] fp32 (natural log; -inf if empty)
  * Arithmetic: both products run on the tensor cores as E4M3 x E4M3 with fp32
  * accumulation, straight from the cached E4M3 codes (the latent is never
- * dequantised).  The bf16 query of each head is split exactly into two E4M3
- * terms, q = s_h (hi + lo), s_h the power of two >= amax_h / 448: exact for
- * every query element at or above 2^-6 s_h, E4M3's smallest normal step (a
- * bf16 has 8 significant bits, hi takes 4, lo the other 4); smaller elements
- * keep an absolute error below 2^-10 s_h (half of E4M3's subnormal step).
- * The RoPE part (fp8_ds_mla) runs as bf16 x bf16.  The softmax is fp32; each
+ * dequantised).  The bf16 query of each head is split into two E4M3
+ * terms, q = s_h (hi + lo), s_h the power of two >= amax_h / 448, amax_h the
+ * head's largest latent element (SML_LATENT_E4M3: or RoPE element): exact for
+ * every element at or above 2^-2 s_h (a bf16 has 8 significant bits, hi takes 4,
+ * lo the other 4 down to E4M3's smallest step, 2^-9); smaller elements are
+ * within half that step, 2^-10 s_h or at most 2^-17.8 amax_h.  The RoPE part (fp8_ds_mla) runs as bf16 x bf16.  The softmax is fp32; each
  * weight 2^(z_i - M_h) * block scale is split into three E4M3 terms whose sum
  * carries 12 significant bits, with M_h a per-head integer exponent that keeps
  * every weight at most 440 and the dominant ones at or above 4 (in E4M3's
@@ -315,7 +315,8 @@ int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
  * where H > 16) that share an exponent.  Which way a small weight is
  * rounded differs from row to row of a tile, so that the tens of thousands
  * behind a dominant key keep their sum: n of them are off by some 2^-20 sqrt(n)
- * of the largest together.  Positions in a page outside the
+ * of the largest together.  A head's query enters an FP8 pool's products as in
+ * sml_sparse_mla_decode: elements below 2^-2 s_h within 2^-10 s_h.  Positions in a page outside the
  * pool are masked (SML_FAULT_PAGE).  An infinity or NaN in a head's query stays
  * in that head.
  * Workspace: SML_STAGE_PAGED.  Nothing in it has to survive between calls; calls

@@ -53,8 +53,7 @@
 //     sixteen warps so that a tile's weights are ready well within the time
 //     the next tile's rows take to arrive: the tile buffer is then free again
 //     before the loaders need it.
-// The query is split exactly into two E4M3 terms sharing a power-of-two scale
-// per head; products of E4M3 values are exact and accumulate in fp32.
+// The query is split into two E4M3 terms sharing a power-of-two scale per head; products of E4M3 values are exact and accumulate in fp32.
 // Every wait is bounded; a wait that gives up sets SML_FAULT_TIMEOUT and the
 // CTA winds down (no trap).
 #include <cuda_bf16.h>
@@ -366,7 +365,8 @@ __device__ __forceinline__ void cur_next(Cur& c, const Params& P, long long ue) 
 // and lo E4M3 and s_h a power of two >= amax_h / 448, so q / s_h, its
 // rounding to hi and the residual lo are exact in fp32, and lo is exact in
 // E4M3 (a bf16 has 8 significant bits, hi takes 4, the residual the other 4)
-// down to E4M3's subnormal step.  RoPE part: copied as bf16; for a plain E4M3
+// from |q| = 2^-2 s_h on; below it is off by at most half of E4M3's subnormal
+// step, 2^-10 s_h.  RoPE part: copied as bf16; for a plain E4M3
 // pool split the same way (its products are E4M3 x E4M3).  A bf16 pool takes
 // the bf16 query as it is (bf16 x bf16 products), s_h = 1.
 template <int kFmt>

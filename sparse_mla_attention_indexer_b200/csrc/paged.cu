@@ -18,7 +18,7 @@
 //     latent dims at a time;
 //   * warp 16 issues S^T = C Q^T (keys as M, heads as N: 16 or 32 heads as M
 //     would waste half of the smallest M and more), straight from the E4M3 codes,
-//     the bf16 query split exactly into two E4M3 terms; one accumulator per block
+//     the bf16 query split into two E4M3 terms; one accumulator per block
 //     scale, RoPE apart in bf16;
 //   * warps 0-15 read S^T (thread = key x a quarter of the heads), scale, take
 //     2^(z - M_h) and write the weights, block scale folded in, as two E4M3
@@ -538,8 +538,10 @@ __device__ __forceinline__ void tmem_stn(uint32_t a, const uint32_t (&r)[8]) { p
 
 // Stage the query of (token t, head group g); thread = head x 1 / kPer of its
 // latent dims and RoPE dims.  E4M3 pools: q = s_h (hi + lo), both E4M3, s_h the
-// power of two with amax_h <= 448 s_h: exact wherever |q| >= 2^-6 s_h (a bf16 has
-// 8 significant bits, four in each term), else within 2^-10 s_h.  RoPE: bf16 as
+// power of two with amax_h <= 448 s_h.  A bf16 has 8 significant bits, four in
+// each term, and lo's step is 2^-9: exact wherever |q| >= 2^-2 s_h; below, within
+// half that step, 2^-10 s_h, 2^-17.8 of amax_h or less (2^-8.8 of an element 2^-9
+// of the largest, a bf16's own rounding; 2^-5 of one 2^-13 of it).  RoPE: bf16 as
 // given (fp8_ds_mla), or split the same way (plain E4M3).  bf16 pools: the bf16
 // query as given.
 template <int kFmt, int kHU>
