@@ -209,7 +209,9 @@ def _p(x) -> int | None:
     try:
         return x.data_ptr()
     except AttributeError:
-        return x   # an address
+        if isinstance(x, int):
+            return x   # an address
+        raise          # (ctypes would take a bytes object's host memory for one)
 
 
 _cuda_ready = False
