@@ -64,16 +64,19 @@ struct MlaWs {
   MlaPlan plan;
 };
 
-// Paged MLA work split.  A unit is (query token, group of kPagedHeads heads,
+// Paged MLA work split.  A unit is (query token, group of paged_heads() heads,
 // tile of two pages); a token has at least one tile, so that a token with
 // nothing to attend to still has a CTA that writes its empty result.  The tile
 // counts follow from device data, so every CTA works out its range itself:
 // head group g is served by the CTAs with blockIdx.x % hg == g, and those share
-// the group's tiles (token-major) in equal contiguous ranges.  A CTA writes a
-// token that lies wholly in its range straight to the output; of the others it
-// holds at most two pieces, one at each end of its range, which go to its two
-// partial slots and are joined by the merge: slot 0 for a piece that does not
-// begin its token, slot 1 for one that does.
+// the group's tiles (token-major) in one of two ways (share() in paged.cu):
+// equal contiguous ranges, or m CTAs to every token, each an equal piece of it.
+// A CTA writes a token that lies wholly in its range straight to the output;
+// pieces of the others go to its two partial slots and are joined by the merge:
+// slot 0 for a piece that does not begin its token, slot 1 for one that does.
+// An equal range holds at most one of each, at its ends; a CTA of the second
+// way has one piece (slot 1 for the first of the m, slot 0 for the others) or,
+// where a token has fewer tiles than m, none.
 struct PagedWs {
   int4* join;          // [ctas] {token, its first CTA, its last, this one} of the token that a CTA continues; token -1: none
   float* part_out;     // [ctas * 2 * heads per unit, 512]
