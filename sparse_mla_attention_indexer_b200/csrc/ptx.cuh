@@ -90,8 +90,20 @@ __device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, c
   }
 }
 
+constexpr uint32_t kWaitUs = 1000000u;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
-                                          uint32_t limit_us = 1000000u) {
+                                          uint32_t limit_us = kWaitUs) {
+#ifdef SML_WAIT_POLLS
+  // For the tests of what follows a wait that gives up: so many polls instead of
+  // a second.  (The waits for copies and products in flight keep their limit.)
+  if (limit_us == kWaitUs) {
+    for (int i = 0; i < SML_WAIT_POLLS; ++i) {
+      if (mbar_test_wait(bar, parity)) return true;
+      if (abort && *abort) return false;
+    }
+    return false;
+  }
+#endif
   if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, abort, limit_us);
 }
