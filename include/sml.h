@@ -308,9 +308,10 @@ int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
  * A token that sees nothing (n_t = 0, or its request's lengths are bad) gets
  * out = 0 and lse = -inf.  What cached rows hold at or past n_t, or before the
  * window, never matters, NaN included.  The products, the row sums and the
- * accumulated outputs are fp32; each softmax weight enters its product with at
- * least 8 significant bits, as a bf16 has, or (FP8 pools) within 2^-18 of the
- * largest of its head where that is more; fp8_ds_mla: within 2^-14, of weight
+ * accumulated outputs are fp32; each softmax weight enters its product with 8
+ * significant bits, as a bf16 has (bf16 pools: 16; FP8 pools: within 1.4 x 2^-8
+ * of itself in all), or (FP8 pools) within 2^-18 of the largest of its head where
+ * that is more; fp8_ds_mla: within 2^-14, of weight
  * over its head's largest times the block's scale, the largest of 4 heads (8
  * where H > 16) that share an exponent.  Which way a small weight is
  * rounded differs from row to row of a tile, so that the tens of thousands

@@ -458,10 +458,14 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float& x0, float& x1) {
   return c;
 }
 // Two weights (at most 448) in half precision as two E4M3 terms, hi + 2^-4 lo:
-// eight significant bits, as many as a bf16 has.  x - hi is exact in half
-// precision and at most 16, so lo stays within 256; the epilogue gives lo's
-// columns of O their 2^-4.  (hi without the conversion back, by Veltkamp's
-// splitting in half precision, measured the same.)
+// eight significant bits, as many as a bf16 has, where the sparse attention's
+// three terms carry twelve.  A third would not fit: 32 heads' O of three terms, 384
+// columns, and their logits, 256, are more than tensor memory's 512.  The three
+// roundings to half precision before (of the weight, the scale and their product,
+// 2^-11 each) let one instruction split two heads' weights; all of it is 1.4 x
+// 2^-8 of a weight at most.  x - hi is exact in half precision and at most 16, so lo stays within 256; the
+// epilogue gives lo's columns of O their 2^-4.  (hi without the conversion back,
+// by Veltkamp's splitting in half precision, measured the same.)
 //
 // Weights below 2^-6 keep lo's subnormal step, 2^-13, and a long context behind a
 // dominant key holds tens of thousands of them, which add up: alike, they would
