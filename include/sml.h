@@ -311,15 +311,17 @@ int sml_noalloc_read_status(int clear, int32_t* bits, void* stream);
  * accumulated outputs are fp32; each softmax weight enters its product with 8
  * significant bits, as a bf16 has (bf16 pools: 16; FP8 pools: within 1.4 x 2^-8
  * of itself in all), or (FP8 pools) within 2^-18 of the largest of its head where
- * that is more; fp8_ds_mla: within 2^-14, of weight
- * over its head's largest times the block's scale, the largest of 4 heads (8
- * where H > 16) that share an exponent.  Which way a small weight is
- * rounded differs from row to row of a tile, so that the tens of thousands
- * behind a dominant key keep their sum: n of them are off by some 2^-20 sqrt(n)
- * of the largest together.  A head's query enters an FP8 pool's products as in
- * sml_sparse_mla_decode: elements below 2^-2 s_h within 2^-10 s_h.  Positions in a page outside the
- * pool are masked (SML_FAULT_PAGE).  An infinity or NaN in a head's query stays
- * in that head.
+ * that is more.  fp8_ds_mla: 4 heads (8 where H > 16) share an exponent for each
+ * block of 128 dims, so there the product of weight and block scale is within
+ * 2^-14 of the largest such product among them, each weight relative to its
+ * head's largest so far; where the block's scales fall along the context (by up
+ * to 2^60 in all) the exponent follows once a head's logits have risen by 8
+ * octaves.  Which way a small weight is rounded differs from row to row of a
+ * tile, so that the tens of thousands behind a dominant key keep their sum: n of
+ * them are off by some 2^-20 sqrt(n) of the largest together.  A head's query
+ * enters an FP8 pool's products as in sml_sparse_mla_decode: elements below 2^-2
+ * s_h within 2^-10 s_h.  Positions in a page outside the pool are masked
+ * (SML_FAULT_PAGE).  An infinity or NaN in a head's query stays in that head.
  * Workspace: SML_STAGE_PAGED.  Nothing in it has to survive between calls; calls
  * that may overlap on the GPU need one each. */
 int sml_paged_mla_decode(const sml_problem* p, const void* q, sml_cache latent, int32_t window, void* out,

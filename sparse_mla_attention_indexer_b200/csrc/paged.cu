@@ -29,17 +29,18 @@
 // sets SML_FAULT_TIMEOUT and the CTA winds down.
 //
 // What bounds it, and what it measured (B200, 6.57 TB/s copy):
-//   * 16 heads, 32 contexts of 8K to 64K tokens: HBM.  143 us for 787 MB, 5.5
-//     TB/s; bf16 rows of the same batch 220 us, 96 % of the copy rate.  A tile
+//   * 16 heads, 32 contexts of 8K to 64K tokens: HBM.  146 us for 787 MB, 5.4
+//     TB/s; bf16 rows of the same batch 226 us, 93 % of the copy rate.  A tile
 //     takes 2.0 us against 1.9 of a 148th of that rate; the rest is what stands
 //     before and after the loop (first loads, uneven finish, join).
 //   * 128 heads, 32 tokens of 60,000 (four groups of 32 heads, which read a tile
-//     from L2 after the first): 906 us, 590 TFLOP/s of the attention's own.  The
-//     two buffers' cycle bounds it, and shared memory under it: of 3,500 to 3,900
-//     cycles a tile the products' operands take 1,930 (a product costs its
-//     operands' bytes / 128 B, 52 cycles at N = 64 whatever their majors), TMA's
-//     writes 660 and the weights 400, and each slows the others (PV takes 2,900
-//     cycles from its first product to its last).  Issue 45 %, L2 35 %.  Twice the
+//     from L2 after the first): 940 us, 570 TFLOP/s of the attention's own.  The
+//     two buffers' cycle bounds it, and probably shared memory under it: of 3,500
+//     to 3,900 cycles a tile the products' operands take 1,930 by the rate of
+//     products timed alone (their operands' bytes / 128 B, 52 cycles at N = 64
+//     whatever their majors; no counter shows it), TMA's writes 660 and the weights
+//     400, and each slows the others (PV takes 2,900 cycles from its first product
+//     to its last).  Issue 46 %, L2 35 %.  Twice the
 //     heads a product would read the tile half as often, but 64 heads' O and
 //     logits do not fit in TMEM, nor a third buffer beside the query and the
 //     weights (224 KB); weights handed to PV in two waves, two loading warps, and
@@ -195,8 +196,8 @@ __device__ __forceinline__ int cta_of(long long total, int used, long long u) { 
 // but the longest token decides.  A piece costs about as much as three tiles
 // more (its query, its first tile, its output), and joining split tokens two.
 // 128 heads (37 CTAs a head group), 32 tokens: over 32 selected blocks, selection
-// included, 49 us with whole tokens and 60 with equal ranges; over 60,000 tokens
-// of context equal ranges are 5 % faster.
+// included, 56 us with whole tokens and 71 with equal ranges; over 60,000 tokens
+// of context equal ranges are 4 % faster.
 __device__ __forceinline__ void share(Range& R, int T, int cpg, int gi, int longest) {
   const long long most = div_ll(R.total + cpg - 1, cpg);
   R.m = T <= cpg ? (int)((unsigned)cpg / (unsigned)T) : 0;
@@ -361,8 +362,7 @@ struct __align__(1024) Smem {
   float sc[F::kDs ? F::kBufs : 1][kKT][4];        // [buffer][key] block scales
   __align__(8) float xmax[4][4][kHU / 4];                      // [head quarter][key quarter][head]
   __align__(16) float xscale[4][4][4];            // [head quarter][key quarter][block]
-  float ebtop[16][4];                             // [warp][block] and risen [warp]: see rebase
-  int risen[16];
+  float mlook[16][kHU / 4], ebtop[16][4];         // [warp][head], [warp][block]: see rebase
   __align__(8) float nm[16][kHU / 4], fac[16][kHU / 4];   // [warp][head] -M_h, and what O scales by
   __align__(8) float xsum[4][4][kHU / 4];
   float qs[kHU];                                  // power-of-two query scale per head
@@ -663,12 +663,13 @@ __device__ __forceinline__ float log_rel(const float (&sc)[4], const float (&ebf
 // integer M_h that puts it in (56, 112]: headroom of 4 for later tiles, and the
 // dominant weights keep all eight bits.  Then the same for each block's weight
 // times scale, over the quarter's heads: eb rises where a product passes the cap,
-// and else, once every M_h has risen by two octaves (`risen`, since the last time),
+// and else, once some M_h has risen by kLook octaves since the last look (mlook),
 // falls to what this tile's largest product needs, so that scales that fall while
-// M_h rises keep their bits.  (Each time at all: 1 to 4 % more in the verification
-// step.)  What O holds grows as eb falls: within kFall octaves of the largest eb so
-// far (ebtop, less what every M_h has risen by since) O stays below 2^112, 2^30 keys
-// of 440 x 448 each.  O scales by powers of two, exactly.
+// logits rise keep their bits.  Heads whose logits fall do not hold it.  (A look at
+// every rise takes 4 to 7 % more time in the verification step, after 4 octaves 2
+// to 5 %, after 8 1 %.)  What O holds grows as eb falls: within kFall octaves of
+// the largest eb so far (ebtop, less what every M_h has risen by since) O stays
+// below 2^112, 2^30 keys of 440 x 448 each.  O scales by powers of two, exactly.
 //
 // In: z the logits + lk; out: z less M_h.  last: the tile whose PV O waits for;
 // -1 where O holds nothing yet.  False: that wait gave up (every warp takes part
@@ -678,7 +679,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
                                        const float (&scv)[4], float (&ebf)[4], float& lk, uint32_t T0, int last) {
   using F = Fmt<kFmt>;
   constexpr int kHT = kHU / 4, kFirst = 1000;
-  constexpr float kFall = 64.f;
+  constexpr float kLook = 8.f, kFall = 64.f;
   constexpr float kLimit = F::kDs ? kHead<kFmt> + 1.f : kCap<kFmt>;   // (the block's scale may come on top)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, hq = warp >> 2;
   // this thread's latent dim of output block 0, this quarter's heads
@@ -694,7 +695,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
     if (lane == 0) *reinterpret_cast<float2*>(&S.xmax[hq][q4][2 * i]) = make_float2(a, b);
   }
   group_sync(hq);
-  int rise;   // the least that any of the quarter's M_h rises by
+  bool look = false;   // whether some M_h has risen by kLook octaves since eb was looked at (or is new)
   {
     const int h = lane % kHT;
     const float e = fmaxf(fmaxf(S.xmax[hq][0][h], S.xmax[hq][1][h]), fmaxf(S.xmax[hq][2][h], S.xmax[hq][3][h]));
@@ -710,7 +711,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       S.nm[warp][h] = neg;
       S.fac[warp][h] = was ? pow2(-by) : 1.f;
     }
-    rise = __reduce_min_sync(0xffffffffu, was && neg > -INFINITY ? by : kFirst);   // (an infinite M_h: a head of NaN)
+    if constexpr (F::kDs) look = __any_sync(0xffffffffu, -neg - S.mlook[warp][h] >= kLook);
     const bool any = __any_sync(0xffffffffu, was && by > 0);   // (also makes the stores visible to the warp)
     __syncwarp();
 #pragma unroll
@@ -742,8 +743,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
     float u = -kFar;
 #pragma unroll
     for (int i = 0; i < kHP; ++i) u = fmaxf(u, fmaxf(z[i].x, z[i].y));
-    int risen = rise == kFirst ? kFirst : S.risen[warp] + rise;
-    if (risen >= 2 || group_any(hq, u + lk > kCap<kFmt>)) {
+    if (look || group_any(hq, u + lk > kCap<kFmt>)) {
       float v[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) v[b] = ptx::warp_max_f32(u + lg2(scv[b]));
@@ -754,13 +754,16 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       const float was = b & 2 ? (b & 1 ? ebf[3] : ebf[2]) : (b & 1 ? ebf[1] : ebf[0]);
       const int eb = 127 - (int)(__float_as_uint(was) >> 23);
       const int fit = (int)ceilf(fminf(fmaxf(t - kHead<kFmt>, -126.f), 126.f));
-      const float top = S.ebtop[warp][b] - (float)risen;
+      // what every M_h has risen by (a head without one, or with an infinite one, aside)
+      const float mh = -S.nm[warp][lane % kHT], ml = S.mlook[warp][lane % kHT], gone = mh - ml;
+      const int rise = __reduce_min_sync(0xffffffffu, ml != kNoM && gone < (float)kFirst ? (int)gone : kFirst);
+      const float top = S.ebtop[warp][b] - (float)rise;
       const int to = rise == kFirst               ? fit
                      : t - (float)eb > kCap<kFmt> ? max(fit, eb)
                      : t > -INFINITY              ? max(min(fit, eb), (int)(top - kFall))
                                                   : eb;   // (scales of 0: nothing to fit)
-      risen = 0;
-      __syncwarp();   // every lane has read the old one
+      __syncwarp();   // every lane has read the old ones
+      if (lane < kHT) S.mlook[warp][lane] = mh;
       if (lane < 4) S.ebtop[warp][b] = rise == kFirst ? (float)to : fmaxf(top, (float)to);
       const float now = pow2(-to);
 #pragma unroll
@@ -784,8 +787,6 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       }
       lk = log_rel(scv, ebf);
     }
-    __syncwarp();
-    if (lane == 0) S.risen[warp] = risen;
 #pragma unroll
     for (int i = 0; i < kHP; ++i) z[i] = __fadd2_rn(z[i], make_float2(lk, lk));
   }
@@ -1098,7 +1099,10 @@ paged_mla_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_const
         nM[i] = make_float2(-kNoM, -kNoM);
         lrow[i] = make_float2(0.f, 0.f);
       }
-      if (lane < kHT) S.nm[warp][lane] = -kNoM;
+      if (lane < kHT) {
+        S.nm[warp][lane] = -kNoM;
+        S.mlook[warp][lane] = kNoM;
+      }
       // A block's scales enter the weights relative to 2^eb, so that every block
       // uses E4M3's range whatever its magnitude; the output is multiplied back.
       float ebf[4] = {1.f, 1.f, 1.f, 1.f};   // 2^-eb

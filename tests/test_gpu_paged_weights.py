@@ -246,3 +246,65 @@ def test_one_head_rises_while_one_blocks_scales_fall(heads, fall):
     wl = rising_case(heads, 3, slice(1, None, 4), fall, False)
     out, lse = run(wl)
     check_block_scales(f"one head, fall {fall}", wl, out, lse, [0, 80, 159])
+
+
+def shared_exponent_term(p, sc, codes, share):
+    """What the weights of an fp8_ds_mla token (one piece) may be off by in all, [H, 512]: six deviations of
+    roundings that differ from key to key, each at most 2^-13 of the unit 2^(M_h + eb_b) of its tile.
+    2^M_h is at most 1 / 56 of the head's largest p so far, 2^eb_b at most 1 / 56 of the largest product
+    (a weight of at most 440 times the block's scale) that the heads which share it have had since eb was
+    last looked at: from then on, 8 octaves of M_h, 10 of a head's largest p (M_h follows within 2)."""
+    H, n = p.shape
+    starts = np.arange(0, n, 128)
+    top = np.maximum(np.stack([p[:, a:a + 128].max(1) for a in starts], 1), 1e-300)          # [H, tiles]
+    run = np.maximum.accumulate(top, 1)
+    prod = np.stack([(p[:, a:a + 128, None] / run[:, i, None, None] * sc[None, a:a + 128]).max(1)
+                     for i, a in enumerate(starts)], 1)                                      # [H, tiles, 4]
+    prod = prod.reshape(-1, share, len(starts), 4).max(1)                                     # [quarters, tiles, 4]
+    tol = np.zeros((H, 4, 128))
+    for g in range(len(prod)):
+        heads = slice(g * share, (g + 1) * share)
+        since, looked = 0, run[heads, 0]
+        for i, a in enumerate(starts):
+            if (run[heads, i] > looked * 2.0 ** 10).any():
+                since, looked = i, run[heads, i]
+            unit = run[heads, i, None] / 56 * prod[g, since:i + 1].max(0) * 440 / 56           # [share, 4]
+            tol[heads] += (2.0 ** -13 * unit[:, :, None]) ** 2 * (codes[a:a + 128] ** 2).sum(0).reshape(4, 128)
+    return 6 * np.sqrt(tol).reshape(H, 512)
+
+
+@pytest.mark.parametrize("large", [8, 16, 30])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_heads_that_fall_do_not_hold_a_blocks_exponent(heads, large):
+    """Half of the heads that share an exponent attend to the first keys, the others' logits rise by 5
+    octaves a tile; one block's scales are 2^large larger in two tiles of the middle.  The rising heads'
+    outputs, which come from the last tiles, keep their bits."""
+    n, new = 2048 + 160, 160
+    wl = synth.make_workload(f"weights/held/{heads}", [n], [new], heads, layers=(("l", 64, False, None),))
+    tile = np.arange(n) // 128
+    pe = np.zeros((n, 64))
+    pe[:, :8] = tile[:, None] / 16
+    put_rows(wl, rows_of(wl, 0, np.arange(n)), latents(n), pe)
+    rows, at = wl.latent.reshape(-1, 656), rows_of(wl, 0, np.arange(n))
+    sc = np.ascontiguousarray(rows[at, 512:528]).view("<f4")
+    sc[(tile == 5) | (tile == 6), 2] *= np.float32(2.0 ** large)
+    rows[at, 512:528] = sc.view(np.uint8)
+    q = np.zeros((new, heads, 576), np.float32)
+    q[:, ::2, 512:520], q[:, 1::2, 512:520] = -6, 5
+    wl.layers[0].q = synth.to_bf16_bits(q)
+    wl.sm_scale = float(np.float32(2 * np.log(2.0)))
+    out, lse = run(wl)
+    n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
+    pages, rws = F.physical(wl.block_table[0], np.arange(n))
+    c, pe = F.latent_rows(wl.latent, pages, rws)
+    sc = PC.block_scales(wl, pages, rws)
+    for t in (0, new - 1):
+        m = int(n_all[t])
+        want, want_lse, tol, ltol = PC.expect(wl, 0, t, np.arange(m))
+        z = wl.sm_scale * (F.decode_bf16(wl.layers[0].q[t])[:, 512:] @ pe[:m].T)
+        p = np.exp(z - want_lse[:, None])
+        A = p @ np.abs(c[:m])
+        d = (ltol - 2.0 ** -20 * (1 + np.abs(want_lse)))[:, None]
+        tol = 2 * d * ((p * (1 - p)) @ np.abs(c[:m])) + PC.U * np.abs(want) + (PC.U + 3 * 2.0 ** -11) * A * 1.01
+        tol += shared_exponent_term(p, sc[:m], c[:m] / np.repeat(sc[:m], 128, 1), 4 if heads == 16 else 8)
+        PC.check(f"large {large} token {t}", out[t], lse[t], (want, want_lse, tol, ltol + (m / 128 + 8) * 2.0 ** -24))
