@@ -34,7 +34,7 @@
 //     takes 2.0 us against 1.9 of a 148th of that rate; the rest is what stands
 //     before and after the loop (first loads, uneven finish, join).
 //   * 128 heads, 32 tokens of 60,000 (four groups of 32 heads, which read a tile
-//     from L2 after the first): 940 us, 570 TFLOP/s of the attention's own.  The
+//     from L2 after the first): 945 us, 566 TFLOP/s of the attention's own.  The
 //     two buffers' cycle bounds it, and probably shared memory under it: of 3,500
 //     to 3,900 cycles a tile the products' operands take 1,930 by the rate of
 //     products timed alone (their operands' bytes / 128 B, 52 cycles at N = 64
@@ -707,6 +707,7 @@ __device__ __forceinline__ bool rebase(Smem<kFmt, kHU>& S, float2 (&z)[kHP], flo
       by = (int)fminf(Mn + neg, 500.f);   // a positive integer (of a head without M_h: any)
       neg = -Mn;
     }
+    __syncwarp();   // every lane has read the old one
     if (lane < kHT) {
       S.nm[warp][h] = neg;
       S.fac[warp][h] = was ? pow2(-by) : 1.f;

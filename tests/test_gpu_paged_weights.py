@@ -179,9 +179,10 @@ def test_several_dominant_keys_and_steps_between_levels(fmt):
 
 
 def check_block_scales(name, wl, out, lse, tokens):
-    """Against the contract for fp8_ds_mla, at half of what it allows: a weight within 2^-15 of V_b = the
-    largest p_hi / pmax_h sc_ib of the heads that share an exponent (4, or 8 of 32 heads and more) over
-    all keys, times its head's pmax_h and its code, and the other terms of the module's bounds."""
+    """Against less than the contract for fp8_ds_mla allows: a weight within 2^-15 of V_b = the largest
+    p_hi / pmax_h sc_ib of the heads that share an exponent (4, or 8 of 32 heads and more) over all keys
+    (the contract: over pmax_h so far), times its head's pmax_h and its code, and the other terms of the
+    module's bounds."""
     n_all = dsa.visible_lengths(wl.cu_q, wl.ctx_len)
     pages, rows = F.physical(wl.block_table[0], np.arange(int(wl.ctx_len[0])))
     c_all, pe_all = F.latent_rows(wl.latent, pages, rows)
